@@ -399,6 +399,93 @@ int moe_walk_plan(const int32_t *counts, const int32_t *order, int n_active, int
 int moe_profile_begin(int n_calls);
 int moe_profile_end(float *ms, int max_calls);
 
+/* ---- MXFP4 experts -------------------------------------------------------------------------
+ *
+ * Rows in microscaled 4-bit floating point ("OCP Microscaling Formats (MX) Specification", MXFP4):
+ * per block of 32 values along the row one scale byte e, standing for 2^(e - 127) (255: the block
+ * is NaN), and 32 codes of 4 bits: sign, then the index of 0, 0.5, 1, 1.5, 2, 3, 4, 6.  Two arrays:
+ *   codes  [rows x n/2] bytes   value 2i in the low nibble of byte i, value 2i + 1 in the high one
+ *   scales [rows x n/32] bytes
+ * A matrix of an expert has its rows along the reduction dimension, as in the other formats, and
+ * the experts' matrices follow each other.  The products run on the matrix cores in this form, so
+ * nothing is repacked.  These entry points stand beside the q8_1 ones: a layer is
+ *   moe_route_topk, moe_build_maps, moe_mxfp4_quantize (each token once; the product gathers rows
+ *   through src, so nothing is scattered), moe_mxfp4_mm_grouped (gate/up with SwiGLU),
+ *   moe_mxfp4_mm_grouped (down, bf16 rows), moe_combine_bf16.
+ * T, rows and the other sizes are at least 1, as everywhere in this interface. */
+
+/* Element types of the entry points that take several. */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
+
+/* x [rows x n], `dtype` values, rows ldx values apart -> codes, scales.  A block's scale is
+ * 2^(floor(log2(amax)) - 2), 2^-127 at least; a value is v / scale (exact) rounded to the nearest
+ * code, ties to the even one, beyond 6 to 6.  The sign of a zero is kept.  A block that holds an
+ * infinity or a NaN gets scale byte 255 and codes 0.  n: a multiple of 32 (else
+ * MOE_EUNSUPPORTED).  x and codes 16-byte aligned, ldx >= n a multiple of 16 bytes (ldx is not
+ * looked at for a single row). */
+int moe_mxfp4_quantize(const void *x, int dtype, int64_t ldx, int rows, int n, void *codes,
+                       void *scales, void *stream);
+
+/* The values that codes and scales stand for, exactly: y [rows x n] in MOE_F32 or MOE_BF16 (MOE_F16,
+ * whose range is smaller, is refused), rows ldy values apart.  Alignment as above. */
+int moe_mxfp4_dequantize(const void *codes, const void *scales, int rows, int n, void *y,
+                         int dtype, int64_t ldy, void *stream);
+
+/* moe_mxfp4_mm_grouped's epilogues */
+typedef enum {
+    MOE_MX_F32 = 0,           /* out = fp32 [rows x n_out] */
+    MOE_MX_BF16 = 1,          /* out = bf16 [rows x n_out], rounded once from the fp32 sums */
+    MOE_MX_SWIGLU_MXFP4 = 2   /* out = codes, out_scales = scales of h = silu(gate) * up, rows of
+                                 n_out values quantised as moe_mxfp4_quantize does */
+} moe_mx_epilogue;
+
+/* The grouped product over every expert in one call: for expert e and its rows r = offsets[e] ..
+ * offsets[e+1]-1 (offsets int32 [E+1], non-decreasing from 0, as moe_build_maps gives them),
+ *   y[r, n] = sum_k A[a(r), k] * W[e, n, k],   a(r) = src ? src[r] / K : r,
+ * products and sums in fp32.  w_codes, w_scales: E matrices of n_out rows of k_in values (2 n_out
+ * rows for MOE_MX_SWIGLU_MXFP4: gate, then up).  a_codes, a_scales: n_act rows of k_in values;
+ * src (int32 [rows], moe_build_maps' src with its K) may be NULL, and K is then not looked at: row r reads
+ * activation row r and n_act >= rows.  rows: the rows that out holds; rows from offsets[E] on
+ * are left as they were.  An a(r) outside [0, n_act) is a caller error that stays in bounds:
+ * the row nearest is read.  n_out a multiple of 32, k_in of 128, E <= MOE_MAX_E (else
+ * MOE_EUNSUPPORTED; so are rows above 2^28 - 32 E); codes and out 16-byte aligned, scales 4-byte. */
+int moe_mxfp4_mm_grouped(const void *w_codes, const void *w_scales, int n_out, int k_in,
+                         const int32_t *offsets, int E, const void *a_codes, const void *a_scales,
+                         int n_act, const int32_t *src, int K, int rows, int epilogue, void *out,
+                         void *out_scales, void *stream);
+
+/* moe_combine over bf16 rows [T*K x H] (the down product's MOE_MX_BF16 rows, half the bytes of
+ * fp32 ones); sums in fp32, out fp32 [T x H].  A slot outside [0, T*K) adds nothing.  H a
+ * multiple of 8, T <= 2^23. */
+int moe_combine_bf16(const void *rows, const int32_t *slot, const float *topk_w, int T, int K,
+                     int H, float *out, void *stream);
+
+/* ---- Router balance ------------------------------------------------------------------------
+ *
+ * The load-balance loss of a top-K router with its per-expert counts.  Over the n tokens with
+ * valid[t] != 0 (valid NULL: every token), p[t] = softmax of the token's E logits, c[e] = routes
+ * topk_idx[t, k] == e (ids outside [0, E) count nowhere):
+ *   f[e] = c[e] / (n K),   prob_mean[e] = (1/n) sum_t p[t, e],   loss = E sum_e f[e] prob_mean[e],
+ * 1 when both are uniform.  counts int32 [E + 1]: c, then n.  With n = 0 all are 0.
+ * A logit of -inf is an expert the token may not take; a valid token with nothing else has p = 0 and
+ * counts in n.  NaN and +inf in a valid row: unspecified (in an invalid one they are not looked
+ * at).  Sums are in fp32 and in an order that depends on the sizes alone: the same call gives
+ * the same bits.  logits: `dtype` values [T x E], rows ld values apart (ld >= E).
+ * ws: moe_balance_workspace_size(T, E) bytes, 4-byte aligned.  E <= MOE_MAX_E, K <= min(E, MOE_MAX_K). */
+size_t moe_balance_workspace_size(int T, int E);   /* 0 for sizes the call would refuse */
+int moe_balance_loss(const void *logits, int dtype, int64_t ld, int T, int E,
+                     const int32_t *topk_idx, int K, const uint8_t *valid, int32_t *counts,
+                     float *prob_mean, float *loss, void *ws, size_t ws_bytes, void *stream);
+
+/* Its gradient (f is a constant of it, the counts having none):
+ *   grad_logits[t, j] = g (E/n) p[t, j] (f[j] - sum_e f[e] p[t, e]),
+ * g = grad_loss[0] (device fp32; NULL: 1), rounded once to `dtype`; 0 for an invalid token.
+ * counts: as moe_balance_loss left them.  grad_logits may be logits itself. */
+int moe_balance_loss_backward(const void *logits, int dtype, int64_t ld, int T, int E,
+                              const int32_t *counts, int K, const uint8_t *valid,
+                              const float *grad_loss, void *grad_logits, int64_t ld_grad,
+                              void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,6 +18,8 @@ LIB_PATH = os.path.join(PKG, "libmoe_prefill.so")
 Q8_0, Q4_1, Q8_0_D4 = 0, 1, 2
 QUANT_PER_ROW, QUANT_D4 = 1, 2
 EPI_F32, EPI_SWIGLU_Q8_1, EPI_I32_BLOCKDOTS = 0, 1, 2
+F32, BF16, F16 = 0, 1, 2
+MX_F32, MX_BF16, MX_SWIGLU_MXFP4 = 0, 1, 2
 WS_COUNTS, WS_OFFSETS, WS_SRC, WS_SLOT, WS_ORDER, WS_NACTIVE, WS_Q8X, WS_GROUPS, WS_HQ8, WS_DM, \
     WS_GROUP_STRIDE, WS_STATUS = range(12)
 N_STAGES = 6
@@ -35,7 +37,7 @@ STATUS = {0: "MOE_OK", -1: "MOE_EINVAL", -2: "MOE_EUNSUPPORTED", -3: "MOE_EWORKS
           -4: "MOE_EHIP", -5: "MOE_ENOMEM"}
 
 # name -> (restype, argtypes); the order of this table is the header's order
-P, I, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+P, I, SZ, L64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
 SIGNATURES = {
     "moe_abi_version": (I, []),
     "moe_strerror": (ctypes.c_char_p, [I]),
@@ -66,6 +68,13 @@ SIGNATURES = {
     "moe_walk_plan": (I, [P, P, I, I, I, P, I, I, I, P, P, P, P, I]),
     "moe_profile_begin": (I, [I]),
     "moe_profile_end": (I, [P, I]),
+    "moe_mxfp4_quantize": (I, [P, I, L64, I, I, P, P, P]),
+    "moe_mxfp4_dequantize": (I, [P, P, I, I, P, I, L64, P]),
+    "moe_mxfp4_mm_grouped": (I, [P, P, I, I, P, I, P, P, I, P, I, I, I, P, P, P]),
+    "moe_combine_bf16": (I, [P, P, P, I, I, I, P, P]),
+    "moe_balance_workspace_size": (SZ, [I, I]),
+    "moe_balance_loss": (I, [P, I, L64, I, I, P, I, P, P, P, P, P, SZ, P]),
+    "moe_balance_loss_backward": (I, [P, I, L64, I, I, P, I, P, P, P, L64, P]),
 }
 
 
@@ -371,3 +380,140 @@ def walk_plan(counts, order, n_active, ring_start, streamed, group_size, n_slots
                             ops.ctypes.data_as(vp), max_ops)
     state["cursor"], state["next_event"] = cur.value, nev.value
     return n, (ops[:n] if n >= 0 else ops[:0]), state
+
+
+# ---- MXFP4, the bf16 combine and the balance loss ---------------------------------------------
+# These take torch tensors whose sizes say the call's, so what the C side cannot see of a tensor is
+# checked here (ValueError): its type, its shape, that it is contiguous (rows of x, values, logits and
+# gradients may be apart) and that all of a call's tensors are on the current device.
+def _dtype(t):
+    import torch
+    d = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
+    if d is None:
+        raise ValueError(f"float32, bfloat16 or float16 is wanted, not {t.dtype}")
+    return d
+
+
+def _want(device, *wants):
+    """wants: (name, tensor or None, dtype or None, shape or None, whole): `whole` a contiguous
+    tensor, otherwise a matrix whose rows are."""
+    import torch
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on the current device are wanted, not on {device}")
+    for name, t, dtype, shape, whole in wants:
+        if t is None:
+            continue
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError(f"{name}: {dtype} is wanted, not {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(shape)} is wanted, not {tuple(t.shape)}")
+        if not (t.is_contiguous() if whole else t.stride(-1) == 1 or t.shape[-1] == 1):
+            raise ValueError(f"{name}: {'a contiguous tensor' if whole else 'contiguous rows'} wanted")
+
+
+def mxfp4_quantize(x, codes, scales, stream=None):
+    """x [rows, n] -> codes uint8 [rows, n / 2], scales uint8 [rows, n / 32]."""
+    import torch
+    rows, n = x.shape
+    _want(x.device, ("x", x, None, None, False), ("codes", codes, torch.uint8, (rows, n // 2), True),
+          ("scales", scales, torch.uint8, (rows, n // 32), True))
+    _check("moe_mxfp4_quantize", lib().moe_mxfp4_quantize(
+        _ptr(x), _dtype(x), x.stride(0), rows, n, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def mxfp4_dequantize(codes, scales, values, stream=None):
+    """The values [rows, n] (float32 or bfloat16) that codes and scales stand for."""
+    import torch
+    rows, n = values.shape
+    _want(values.device, ("values", values, None, None, False),
+          ("codes", codes, torch.uint8, (rows, n // 2), True),
+          ("scales", scales, torch.uint8, (rows, n // 32), True))
+    _check("moe_mxfp4_dequantize", lib().moe_mxfp4_dequantize(
+        _ptr(codes), _ptr(scales), rows, n, _ptr(values), _dtype(values), values.stride(0),
+        _stream(stream)))
+
+
+def mxfp4_mm_grouped(w_codes, w_scales, offsets, a_codes, a_scales, out, src=None, K=1,
+                     out_scales=None, stream=None):
+    """w_codes uint8 [E, N, k / 2], w_scales [E, N, k / 32]; offsets int32 [E + 1]; a_codes
+    [n_act, k / 2], a_scales [n_act, k / 32]; src int32 [rows] or None.  out: float32 or bfloat16
+    [rows, N]; with out_scales uint8 [rows, N / 64] the codes uint8 [rows, N / 4] of the SwiGLU
+    of gate (matrix rows 0 .. N/2 - 1) and up."""
+    import torch
+    E, N, kb = w_codes.shape
+    n_act, rows, k, u8 = a_codes.shape[0], out.shape[0], 2 * kb, torch.uint8
+    n_out = N if out_scales is None else N // 2
+    if out_scales is None:
+        epi = {torch.float32: MX_F32, torch.bfloat16: MX_BF16}.get(out.dtype)
+        if epi is None:
+            raise ValueError(f"out: float32 or bfloat16 is wanted, not {out.dtype}")
+        shape = (rows, N)
+    else:
+        if N % 2:
+            raise ValueError("gate and up have as many rows each: N is even")
+        epi, shape = MX_SWIGLU_MXFP4, (rows, n_out // 2)
+    _want(w_codes.device, ("w_codes", w_codes, u8, None, True),
+          ("w_scales", w_scales, u8, (E, N, k // 32), True),
+          ("offsets", offsets, torch.int32, (E + 1,), True),
+          ("a_codes", a_codes, u8, (n_act, kb), True),
+          ("a_scales", a_scales, u8, (n_act, k // 32), True),
+          ("src", src, torch.int32, (rows,), True),
+          ("out", out, u8 if out_scales is not None else None, shape, True),
+          ("out_scales", out_scales, u8, (rows, n_out // 32), True))
+    _check("moe_mxfp4_mm_grouped", lib().moe_mxfp4_mm_grouped(
+        _ptr(w_codes), _ptr(w_scales), n_out, k, _ptr(offsets), E, _ptr(a_codes), _ptr(a_scales),
+        n_act, _ptr(src), K, rows, epi, _ptr(out), _ptr(out_scales), _stream(stream)))
+
+
+def combine_bf16(rows, slot, topk_w, out, stream=None):
+    """out float32 [T, H] of rows bfloat16 [T * K, H], slot int32 and topk_w float32 [T, K]."""
+    import torch
+    T, K = topk_w.shape
+    H = rows.shape[1]
+    if slot.numel() != T * K:
+        raise ValueError(f"slot: {T * K} values are wanted, not {slot.numel()}")
+    _want(rows.device, ("rows", rows, torch.bfloat16, (T * K, H), True),
+          ("slot", slot, torch.int32, None, True), ("topk_w", topk_w, torch.float32, None, True),
+          ("out", out, torch.float32, (T, H), True))
+    _check("moe_combine_bf16", lib().moe_combine_bf16(_ptr(rows), _ptr(slot), _ptr(topk_w), T, K, H,
+                                                      _ptr(out), _stream(stream)))
+
+
+def balance_workspace_size(T: int, E: int) -> int:
+    return lib().moe_balance_workspace_size(T, E)
+
+
+def balance_loss(logits, topk_idx, counts, prob_mean, loss, ws, valid=None, stream=None):
+    """logits [T, E] and topk_idx int32 [T, K] -> counts int32 [E + 1] (the valid tokens last),
+    prob_mean float32 [E], loss float32 [1]; valid uint8 [T] or None; ws: at least
+    balance_workspace_size(T, E) bytes."""
+    import torch
+    T, E = logits.shape
+    K = topk_idx.shape[1]
+    _want(logits.device, ("logits", logits, None, None, False),
+          ("topk_idx", topk_idx, torch.int32, (T, K), True),
+          ("counts", counts, torch.int32, (E + 1,), True),
+          ("prob_mean", prob_mean, torch.float32, (E,), True),
+          ("loss", loss, torch.float32, (1,), True), ("ws", ws, None, None, True),
+          ("valid", valid, torch.uint8, (T,), True))
+    _check("moe_balance_loss", lib().moe_balance_loss(
+        _ptr(logits), _dtype(logits), logits.stride(0), T, E, _ptr(topk_idx), K, _ptr(valid),
+        _ptr(counts), _ptr(prob_mean), _ptr(loss), _ptr(ws), ws.numel() * ws.element_size(),
+        _stream(stream)))
+
+
+def balance_loss_backward(logits, counts, K, grad_logits, valid=None, grad_loss=None, stream=None):
+    """grad_logits [T, E] in logits' type, from balance_loss's counts and grad_loss float32 [1]
+    (None: 1)."""
+    import torch
+    T, E = logits.shape
+    _want(logits.device, ("logits", logits, None, None, False),
+          ("counts", counts, torch.int32, (E + 1,), True),
+          ("grad_logits", grad_logits, logits.dtype, (T, E), False),
+          ("grad_loss", grad_loss, torch.float32, (1,), True),
+          ("valid", valid, torch.uint8, (T,), True))
+    _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
+        _ptr(logits), _dtype(logits), logits.stride(0), T, E, _ptr(counts), K, _ptr(valid),
+        _ptr(grad_loss), _ptr(grad_logits), grad_logits.stride(0), _stream(stream)))
