@@ -447,8 +447,11 @@ typedef enum {
  * src (int32 [rows], moe_build_maps' src with its K) may be NULL, and K is then not looked at: row r reads
  * activation row r and n_act >= rows.  rows: the rows that out holds; rows from offsets[E] on
  * are left as they were.  An a(r) outside [0, n_act) is a caller error that stays in bounds:
- * the row nearest is read.  n_out a multiple of 32, k_in of 128, E <= MOE_MAX_E (else
- * MOE_EUNSUPPORTED; so are rows above 2^28 - 32 E); codes and out 16-byte aligned, scales 4-byte. */
+ * the row nearest is read.  The order of the fp32 sums depends on the sizes alone.
+ * codes and out 16-byte aligned, scales 4-byte (else MOE_EINVAL; 16-byte aligned scales are faster where
+ * k_in is a multiple of 512).  MOE_EUNSUPPORTED: n_out not a multiple of 32 or above 2^21, k_in not one of 128,
+ * E > MOE_MAX_E, K > MOE_MAX_K, an expert's codes or a_codes of 4 GiB or more, rows above 2^28 - 32 E,
+ * (rows / 32 + E) (n_out / 32) of 2^31 or more. */
 int moe_mxfp4_mm_grouped(const void *w_codes, const void *w_scales, int n_out, int k_in,
                          const int32_t *offsets, int E, const void *a_codes, const void *a_scales,
                          int n_act, const int32_t *src, int K, int rows, int epilogue, void *out,

@@ -33,27 +33,28 @@ struct Elem<kF16> {
   typedef _Float16 type;
 };
 
-// The scale byte of a block whose largest magnitude has these bits (sign cleared).
-__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
-  const uint32_t ef = amax_bits >> 23;
+// The scale byte of a block with this largest magnitude.
+__device__ __forceinline__ uint32_t mx_scale_byte(float amax) {
+  const uint32_t ef = __float_as_uint(amax) >> 23 & 255u;
   return ef == 255u ? 255u : (ef > 2u ? ef - 2u : 0u);
 }
 
-// 1 / scale as fp32: 2^(127 - byte), in fp32's normal range for the bytes 0..252 that a finite block
-// has.  For 255 it is of no use: the caller clears a NaN block's codes.
-__device__ __forceinline__ float mx_inverse_scale(uint32_t byte) {
-  return __uint_as_float((254u - byte) << 23);
+// The larger magnitude of two or three values; a NaN among them gives NaN.
+__device__ __forceinline__ float mx_amax(float m, float v) {
+  return __builtin_elementwise_maximum(m, fabsf(v));
 }
 
-// The 8 codes (value i in nibble i) of 8 values already divided by their block's scale.
-// v_cvt_scalef32_pk_fp4_f32 rounds to the nearest, ties to even, and gives 6 beyond 6.
-__device__ __forceinline__ uint32_t mx_codes8(const float (&q)[8]) {
+// The 8 codes (value i in nibble i) of 8 values of a block with this scale byte.
+// v_cvt_scalef32_pk_fp4_f32 divides by the power of two that its scale operand's exponent field stands for
+// (0: 2^-127), rounds to the nearest, ties to even, and gives 6 beyond 6; tested for every border and scale.
+__device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], uint32_t byte) {
+  const float scale = __uint_as_float(byte << 23);
   uint32_t w = 0;
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[0], q[1], 1.0f, 0);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[2], q[3], 1.0f, 1);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[4], q[5], 1.0f, 2);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[6], q[7], 1.0f, 3);
-  return w;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], scale, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], scale, 3);
+  return byte == 255u ? 0u : w;
 }
 
 hipError_t launch_mx_quantize(const void* x, int dtype, int64_t ldx, int rows, int n,
@@ -72,6 +73,7 @@ struct MxProblem {
   uint8_t* out_scales;     // SwiGLU: the requantised rows' scale bytes
   int n_out;               // output columns
   int k_in, E, n_act, K, rows;
+  uint32_t k_mul, k_shift;  // division by K (set by the launcher)
   int epilogue;            // kMxF32, kMxBF16, kMxSwiglu (n_mat = 2 n_out: gate, then up)
 };
 constexpr int kMxF32 = 0, kMxBF16 = 1, kMxSwiglu = 2;

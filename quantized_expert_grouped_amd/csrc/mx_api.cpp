@@ -66,13 +66,20 @@ int moe_mxfp4_mm_grouped(const void* w_codes, const void* w_scales, int n_out, i
                          int n_act, const int32_t* src, int K, int rows, int epilogue, void* out,
                          void* out_scales, void* stream) {
   if (!w_codes || !w_scales || !offsets || !a_codes || !a_scales || !out) return MOE_EINVAL;
-  if (n_out < 1 || k_in < 1 || E < 1 || rows < 1 || n_act < 1 || K < 1) return MOE_EINVAL;
+  if (n_out < 1 || k_in < 1 || E < 1 || rows < 1 || n_act < 1 || (src && K < 1))
+    return MOE_EINVAL;
   if (epilogue < MOE_MX_F32 || epilogue > MOE_MX_SWIGLU_MXFP4) return MOE_EINVAL;
   if (epilogue == MOE_MX_SWIGLU_MXFP4 && !out_scales) return MOE_EINVAL;
   if (!src && n_act < rows) return MOE_EINVAL;
   if (n_out % 32 != 0 || k_in % 128 != 0 || E > MOE_MAX_E) return MOE_EUNSUPPORTED;
-  // the grid: a number per tile of rows by one per 32 columns
-  if (rows / 32 + E > kMaxGroups || n_out / 32 > 65535) return MOE_EUNSUPPORTED;
+  if (src && K > MOE_MAX_K) return MOE_EUNSUPPORTED;
+  // tiles are numbered in 31 bits, a grid's y holds 16, and rows are addressed by 32-bit offsets from an
+  // expert's matrix and from a_codes
+  const int64_t mats = epilogue == MOE_MX_SWIGLU_MXFP4 ? 2 : 1;
+  if (rows / 32 + E > kMaxGroups || n_out / 32 > 65535 ||
+      ((int64_t)rows / 32 + E) * (n_out / 32) >= (int64_t)1 << 31 ||
+      mats * n_out * (k_in / 2) >= (int64_t)1 << 32 || (int64_t)n_act * (k_in / 2) >= (int64_t)1 << 32)
+    return MOE_EUNSUPPORTED;
   if (!aligned(w_codes, 16) || !aligned(a_codes, 16) || !aligned(w_scales, 4) ||
       !aligned(a_scales, 4) || !aligned(out, 16))
     return MOE_EINVAL;
@@ -89,7 +96,7 @@ int moe_mxfp4_mm_grouped(const void* w_codes, const void* w_scales, int n_out, i
   p.k_in = k_in;
   p.E = E;
   p.n_act = n_act;
-  p.K = K;
+  p.K = src ? K : 1;
   p.rows = rows;
   p.epilogue = epilogue;
   return status_of(launch_mx_mm(p, as_stream(stream)));

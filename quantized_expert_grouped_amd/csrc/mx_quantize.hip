@@ -2,8 +2,7 @@
 //
 // Both kernels move each byte once and are bound by memory.  A lane owns 8 values: 16 or 32 bytes
 // in, one dword of codes, so a block of 32 is a quad of lanes whose largest magnitude takes two DPP
-// steps, on integers (the order of non-negative floats is that of their bits, and infinities and NaN
-// come out above every finite value).
+// steps.
 #include "mx.hpp"
 
 namespace moe {
@@ -12,6 +11,9 @@ namespace {
 
 constexpr int kDppXor1 = 0xB1;  // quad_perm [1, 0, 3, 2]
 constexpr int kDppXor2 = 0x4E;  // quad_perm [2, 3, 0, 1]
+
+#define quad(v, ctrl) \
+  __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xF, 0xF, false))
 
 template <int DT>
 __device__ __forceinline__ void load8(const void* base, int64_t i, float (&v)[8]) {
@@ -38,17 +40,13 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* __restrict
   if (i >= n) return;  // whole quads: n is a multiple of 32
   float v[8];
   load8<DT>(x, row * ldx + i, v);
-  uint32_t m = 0;
+  float m = fabsf(v[0]);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppXor1, 0xF, 0xF, false));
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppXor2, 0xF, 0xF, false));
+  for (int j = 1; j < 8; ++j) m = mx_amax(m, v[j]);
+  m = mx_amax(m, quad(m, kDppXor1));
+  m = mx_amax(m, quad(m, kDppXor2));
   const uint32_t byte = mx_scale_byte(m);
-  const float inv = mx_inverse_scale(byte);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] *= inv;
-  uint32_t w = mx_codes8(v);
-  if (byte == 255u) w = 0;
+  const uint32_t w = mx_codes8(v, byte);
   const int64_t at = row * n + i;
   *reinterpret_cast<uint32_t*>(codes + at / 2) = w;
   if ((threadIdx.x & 3) == 0) scales[at / kMxBlock] = (uint8_t)byte;

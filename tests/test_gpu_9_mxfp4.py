@@ -149,7 +149,12 @@ SHAPES = [  # T, K, E, N, k, gather, skew
     (5, 3, 40, 160, 2048, True, 0.0), (40, 2, 4, 128, 128, False, 0.0), (33, 1, 1, 224, 640, True, 0.0),
     (130, 4, 16, 256, 512, True, 0.7), (300, 1, 3, 288, 896, False, 1.5), (257, 6, 64, 64, 1024, True, 0.2),
     (64, 8, 2048, 32, 128, True, 0.0), (700, 2, 3, 512, 256, True, 3.0), (1000, 1, 1, 384, 1152, False, 0.0),
-    (1600, 4, 16, 320, 384, True, 0.1), (2500, 2, 9, 128, 640, False, 0.4)]
+    (1600, 4, 16, 320, 384, True, 0.1), (2500, 2, 9, 128, 640, False, 0.4),
+    # the wide kernel's three tiles, with scale bytes in pieces of 16 and of 4, a last stage of 128
+    # values, and columns that end inside a tile
+    (900, 2, 40, 512, 512, True, 0.5), (900, 2, 40, 544, 128, False, 0.5),
+    (2048, 4, 64, 2048, 512, True, 0.3), (2051, 4, 64, 2080, 640, False, 0.3),
+    (2047, 4, 16, 2080, 1024, True, 0.5), (2048, 4, 16, 2048, 384, True, 2.0)]
 
 
 @pytest.mark.parametrize("epi", [abi.MX_F32, abi.MX_BF16, abi.MX_SWIGLU_MXFP4])
@@ -182,10 +187,38 @@ def test_mm_grouped(T, K, E, N, k, gather, skew, epi):
     mxref.check_codes(host(out), host(os_), h, dh)
 
 
-def test_mm_rows_past_the_experts_are_left_alone():
+def test_mm_scales_at_any_4_byte_address():
+    """Scales that are 4-byte aligned only: the same bytes come out as with aligned ones."""
+    rng = np.random.default_rng(6)
+    T, K, E, N, k = 2000, 2, 30, 512, 512
+    _, maps = gpu_maps(routes(rng, T, K, E, 0.2), E, 0)
+    wc, ws = weights(rng, E, N, k)
+    ac, as_ = mxref.encode(rng.standard_normal((T, k)))
+    wc, ac = dev(wc), dev(ac)
+
+    def at(a, skip):
+        t = torch.empty(a.size + 16, dtype=torch.uint8, device="cuda")[skip:skip + a.size].view(a.shape)
+        return t.copy_(dev(a))
+
+    outs = []
+    for w_skip, a_skip in ((0, 0), (4, 0), (0, 8), (12, 4)):
+        out = empty((T * K, N), torch.float32)
+        note(f"mm scales at {w_skip} {a_skip}")
+        abi.mxfp4_mm_grouped(wc, at(ws, w_skip), maps["offsets"], ac, at(as_, a_skip), out,
+                             src=maps["src"], K=K)
+        outs.append(out)
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
+    for skip in (1, 2):
+        with pytest.raises(abi.MoeError):
+            abi.mxfp4_mm_grouped(wc, at(ws, skip), maps["offsets"], ac, at(as_, 0), outs[0],
+                                 src=maps["src"], K=K)
+
+
+@pytest.mark.parametrize("T,K,E,N,k", [(50, 3, 6, 64, 256), (3000, 3, 50, 640, 256),
+                                       (3000, 3, 70, 2048, 256), (3000, 3, 30, 2048, 256)])
+def test_mm_rows_past_the_experts_are_left_alone(T, K, E, N, k):
     """Routes to ids outside [0, E) take rows past offsets[E]: those keep their bytes, in every epilogue."""
     rng = np.random.default_rng(3)
-    T, K, E, N, k = 50, 3, 6, 64, 256
     idx = routes(rng, T, K, E, 0.0)
     idx.reshape(-1)[::7] = np.array([-1, E, 99])[np.arange(len(idx.reshape(-1)[::7])) % 3]
     _, maps = gpu_maps(idx, E, 0)

@@ -79,7 +79,9 @@ def test_mm_host_checks():
                 dict(a=p + 4), dict(ws=p + 2), dict(as_=p + 1), dict(out=p + 8)):
         assert call(**bad) == -1, bad
     for bad in (dict(n=48), dict(k=192), dict(E=2049), dict(n=32 << 16),
-                dict(rows=1 << 28, n_act=1 << 28)):
+                dict(rows=1 << 28, n_act=1 << 28), dict(src=p, K=65), dict(n=1 << 20, k=1 << 13),
+                dict(n=1 << 19, k=1 << 13, epi=2, outs=p), dict(n_act=1 << 25, k=256),
+                dict(rows=1 << 27, n_act=1 << 27, k=128, n=1 << 14)):
         assert call(**bad) == -2, bad
 
 
