@@ -385,54 +385,79 @@ def walk_plan(counts, order, n_active, ring_start, streamed, group_size, n_slots
 # ---- MXFP4, the bf16 combine and the balance loss ---------------------------------------------
 # These take torch tensors whose sizes say the call's, so what the C side cannot see of a tensor is
 # checked here (ValueError): its type, its shape, that it is contiguous (rows of x, values, logits and
-# gradients may be apart) and that all of a call's tensors are on the current device.
+# gradients may be apart) and that all of a call's tensors are on the current device.  A call on a
+# few rows is bound by the host, so the checks are one pass over the tensors.
+_torch = None
+
+
+def _dtypes():
+    global _torch, _DT
+    if _torch is None:
+        import torch
+        _torch, _DT = torch, {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+    return _DT
+
+
 def _dtype(t):
-    import torch
-    d = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
+    d = _dtypes().get(t.dtype)
     if d is None:
         raise ValueError(f"float32, bfloat16 or float16 is wanted, not {t.dtype}")
     return d
 
 
-def _want(device, *wants):
-    """wants: (name, tensor or None, dtype or None, shape or None, whole): `whole` a contiguous
-    tensor, otherwise a matrix whose rows are."""
-    import torch
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on the current device are wanted, not on {device}")
-    for name, t, dtype, shape, whole in wants:
+def _on_current(t) -> int:
+    """The current device's number, which has to be the tensor's."""
+    _dtypes()
+    device = t.get_device()
+    if device < 0 or device != _torch.cuda.current_device():
+        raise ValueError(f"tensors on the current device are wanted, not on {t.device}")
+    return device
+
+
+def _want(device: int, *wants) -> None:
+    """wants: (name, tensor or None, dtype, shape), contiguous tensors."""
+    for name, t, dtype, shape in wants:
         if t is None:
             continue
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
-        if dtype is not None and t.dtype != dtype:
-            raise ValueError(f"{name}: {dtype} is wanted, not {t.dtype}")
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"{name}: shape {tuple(shape)} is wanted, not {tuple(t.shape)}")
-        if not (t.is_contiguous() if whole else t.stride(-1) == 1 or t.shape[-1] == 1):
-            raise ValueError(f"{name}: {'a contiguous tensor' if whole else 'contiguous rows'} wanted")
+        if t.dtype != dtype or t.shape != shape or t.get_device() != device:
+            raise ValueError(f"{name}: {dtype} {tuple(shape)} on device {device} is wanted, not "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: a contiguous tensor is wanted")
+
+
+def _row_stride(name: str, t, device: int) -> int:
+    """The distance between a matrix's rows, which are contiguous each."""
+    if t.get_device() != device or (t.stride(1) != 1 and t.shape[1] != 1):
+        raise ValueError(f"{name}: a matrix of contiguous rows on device {device} is wanted")
+    return t.stride(0)
+
+
+def _current_stream(stream, device: int):
+    # torch.cuda.current_stream() builds a Stream object, 2.8 us of a call that takes 6
+    return _torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def mxfp4_quantize(x, codes, scales, stream=None):
     """x [rows, n] -> codes uint8 [rows, n / 2], scales uint8 [rows, n / 32]."""
-    import torch
+    dt, dev = _dtype(x), _on_current(x)
     rows, n = x.shape
-    _want(x.device, ("x", x, None, None, False), ("codes", codes, torch.uint8, (rows, n // 2), True),
-          ("scales", scales, torch.uint8, (rows, n // 32), True))
+    u8 = _torch.uint8
+    _want(dev, ("codes", codes, u8, (rows, n // 2)), ("scales", scales, u8, (rows, n // 32)))
     _check("moe_mxfp4_quantize", lib().moe_mxfp4_quantize(
-        _ptr(x), _dtype(x), x.stride(0), rows, n, _ptr(codes), _ptr(scales), _stream(stream)))
+        x.data_ptr(), dt, _row_stride("x", x, dev), rows, n, codes.data_ptr(), scales.data_ptr(),
+        _current_stream(stream, dev)))
 
 
 def mxfp4_dequantize(codes, scales, values, stream=None):
     """The values [rows, n] (float32 or bfloat16) that codes and scales stand for."""
-    import torch
+    dt, dev = _dtype(values), _on_current(values)
     rows, n = values.shape
-    _want(values.device, ("values", values, None, None, False),
-          ("codes", codes, torch.uint8, (rows, n // 2), True),
-          ("scales", scales, torch.uint8, (rows, n // 32), True))
+    u8 = _torch.uint8
+    _want(dev, ("codes", codes, u8, (rows, n // 2)), ("scales", scales, u8, (rows, n // 32)))
     _check("moe_mxfp4_dequantize", lib().moe_mxfp4_dequantize(
-        _ptr(codes), _ptr(scales), rows, n, _ptr(values), _dtype(values), values.stride(0),
-        _stream(stream)))
+        codes.data_ptr(), scales.data_ptr(), rows, n, values.data_ptr(), dt,
+        _row_stride("values", values, dev), _current_stream(stream, dev)))
 
 
 def mxfp4_mm_grouped(w_codes, w_scales, offsets, a_codes, a_scales, out, src=None, K=1,
@@ -441,44 +466,45 @@ def mxfp4_mm_grouped(w_codes, w_scales, offsets, a_codes, a_scales, out, src=Non
     [n_act, k / 2], a_scales [n_act, k / 32]; src int32 [rows] or None.  out: float32 or bfloat16
     [rows, N]; with out_scales uint8 [rows, N / 64] the codes uint8 [rows, N / 4] of the SwiGLU
     of gate (matrix rows 0 .. N/2 - 1) and up."""
-    import torch
+    dev = _on_current(w_codes)
     E, N, kb = w_codes.shape
-    n_act, rows, k, u8 = a_codes.shape[0], out.shape[0], 2 * kb, torch.uint8
-    n_out = N if out_scales is None else N // 2
+    n_act, rows = a_codes.shape[0], out.shape[0]
+    u8, i32 = _torch.uint8, _torch.int32
     if out_scales is None:
-        epi = {torch.float32: MX_F32, torch.bfloat16: MX_BF16}.get(out.dtype)
-        if epi is None:
-            raise ValueError(f"out: float32 or bfloat16 is wanted, not {out.dtype}")
-        shape = (rows, N)
+        epi, n_out, dt, shape = MX_F32, N, out.dtype, (rows, N)
+        if dt == _torch.bfloat16:
+            epi = MX_BF16
+        elif dt != _torch.float32:
+            raise ValueError(f"out: float32 or bfloat16 is wanted, not {dt}")
     else:
         if N % 2:
             raise ValueError("gate and up have as many rows each: N is even")
-        epi, shape = MX_SWIGLU_MXFP4, (rows, n_out // 2)
-    _want(w_codes.device, ("w_codes", w_codes, u8, None, True),
-          ("w_scales", w_scales, u8, (E, N, k // 32), True),
-          ("offsets", offsets, torch.int32, (E + 1,), True),
-          ("a_codes", a_codes, u8, (n_act, kb), True),
-          ("a_scales", a_scales, u8, (n_act, k // 32), True),
-          ("src", src, torch.int32, (rows,), True),
-          ("out", out, u8 if out_scales is not None else None, shape, True),
-          ("out_scales", out_scales, u8, (rows, n_out // 32), True))
+        epi, n_out, dt, shape = MX_SWIGLU_MXFP4, N // 2, u8, (rows, N // 4)
+    _want(dev, ("w_codes", w_codes, u8, (E, N, kb)), ("w_scales", w_scales, u8, (E, N, kb // 16)),
+          ("offsets", offsets, i32, (E + 1,)), ("a_codes", a_codes, u8, (n_act, kb)),
+          ("a_scales", a_scales, u8, (n_act, kb // 16)), ("src", src, i32, (rows,)),
+          ("out", out, dt, shape), ("out_scales", out_scales, u8, (rows, n_out // 32)))
     _check("moe_mxfp4_mm_grouped", lib().moe_mxfp4_mm_grouped(
-        _ptr(w_codes), _ptr(w_scales), n_out, k, _ptr(offsets), E, _ptr(a_codes), _ptr(a_scales),
-        n_act, _ptr(src), K, rows, epi, _ptr(out), _ptr(out_scales), _stream(stream)))
+        w_codes.data_ptr(), w_scales.data_ptr(), n_out, 2 * kb, offsets.data_ptr(), E,
+        a_codes.data_ptr(), a_scales.data_ptr(), n_act, _ptr(src), K, rows, epi, out.data_ptr(),
+        _ptr(out_scales), _current_stream(stream, dev)))
 
 
 def combine_bf16(rows, slot, topk_w, out, stream=None):
-    """out float32 [T, H] of rows bfloat16 [T * K, H], slot int32 and topk_w float32 [T, K]."""
-    import torch
+    """out float32 [T, H] of rows bfloat16 [T * K, H], slot int32 (T * K values) and topk_w
+    float32 [T, K]."""
+    dev = _on_current(rows)
     T, K = topk_w.shape
     H = rows.shape[1]
+    f32 = _torch.float32
     if slot.numel() != T * K:
         raise ValueError(f"slot: {T * K} values are wanted, not {slot.numel()}")
-    _want(rows.device, ("rows", rows, torch.bfloat16, (T * K, H), True),
-          ("slot", slot, torch.int32, None, True), ("topk_w", topk_w, torch.float32, None, True),
-          ("out", out, torch.float32, (T, H), True))
-    _check("moe_combine_bf16", lib().moe_combine_bf16(_ptr(rows), _ptr(slot), _ptr(topk_w), T, K, H,
-                                                      _ptr(out), _stream(stream)))
+    _want(dev, ("rows", rows, _torch.bfloat16, (T * K, H)),
+          ("slot", slot, _torch.int32, slot.shape), ("topk_w", topk_w, f32, (T, K)),
+          ("out", out, f32, (T, H)))
+    _check("moe_combine_bf16", lib().moe_combine_bf16(
+        rows.data_ptr(), slot.data_ptr(), topk_w.data_ptr(), T, K, H, out.data_ptr(),
+        _current_stream(stream, dev)))
 
 
 def balance_workspace_size(T: int, E: int) -> int:
@@ -489,31 +515,30 @@ def balance_loss(logits, topk_idx, counts, prob_mean, loss, ws, valid=None, stre
     """logits [T, E] and topk_idx int32 [T, K] -> counts int32 [E + 1] (the valid tokens last),
     prob_mean float32 [E], loss float32 [1]; valid uint8 [T] or None; ws: at least
     balance_workspace_size(T, E) bytes."""
-    import torch
+    dt, dev = _dtype(logits), _on_current(logits)
     T, E = logits.shape
     K = topk_idx.shape[1]
-    _want(logits.device, ("logits", logits, None, None, False),
-          ("topk_idx", topk_idx, torch.int32, (T, K), True),
-          ("counts", counts, torch.int32, (E + 1,), True),
-          ("prob_mean", prob_mean, torch.float32, (E,), True),
-          ("loss", loss, torch.float32, (1,), True), ("ws", ws, None, None, True),
-          ("valid", valid, torch.uint8, (T,), True))
+    i32, f32 = _torch.int32, _torch.float32
+    _want(dev, ("topk_idx", topk_idx, i32, (T, K)), ("counts", counts, i32, (E + 1,)),
+          ("prob_mean", prob_mean, f32, (E,)), ("loss", loss, f32, (1,)),
+          ("ws", ws, ws.dtype, ws.shape), ("valid", valid, _torch.uint8, (T,)))
     _check("moe_balance_loss", lib().moe_balance_loss(
-        _ptr(logits), _dtype(logits), logits.stride(0), T, E, _ptr(topk_idx), K, _ptr(valid),
-        _ptr(counts), _ptr(prob_mean), _ptr(loss), _ptr(ws), ws.numel() * ws.element_size(),
-        _stream(stream)))
+        logits.data_ptr(), dt, _row_stride("logits", logits, dev), T, E, topk_idx.data_ptr(), K,
+        _ptr(valid), counts.data_ptr(), prob_mean.data_ptr(), loss.data_ptr(), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _current_stream(stream, dev)))
 
 
 def balance_loss_backward(logits, counts, K, grad_logits, valid=None, grad_loss=None, stream=None):
     """grad_logits [T, E] in logits' type, from balance_loss's counts and grad_loss float32 [1]
     (None: 1)."""
-    import torch
+    dt, dev = _dtype(logits), _on_current(logits)
     T, E = logits.shape
-    _want(logits.device, ("logits", logits, None, None, False),
-          ("counts", counts, torch.int32, (E + 1,), True),
-          ("grad_logits", grad_logits, logits.dtype, (T, E), False),
-          ("grad_loss", grad_loss, torch.float32, (1,), True),
-          ("valid", valid, torch.uint8, (T,), True))
+    if grad_logits.dtype != logits.dtype or grad_logits.shape != logits.shape:
+        raise ValueError(f"grad_logits: {logits.dtype} {(T, E)} is wanted, not "
+                         f"{grad_logits.dtype} {tuple(grad_logits.shape)}")
+    _want(dev, ("counts", counts, _torch.int32, (E + 1,)),
+          ("grad_loss", grad_loss, _torch.float32, (1,)), ("valid", valid, _torch.uint8, (T,)))
     _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
-        _ptr(logits), _dtype(logits), logits.stride(0), T, E, _ptr(counts), K, _ptr(valid),
-        _ptr(grad_loss), _ptr(grad_logits), grad_logits.stride(0), _stream(stream)))
+        logits.data_ptr(), dt, _row_stride("logits", logits, dev), T, E, counts.data_ptr(), K,
+        _ptr(valid), _ptr(grad_loss), grad_logits.data_ptr(),
+        _row_stride("grad_logits", grad_logits, dev), _current_stream(stream, dev)))
