@@ -74,16 +74,16 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint8_t* __res
                       : byte == 0u ? __uint_as_float(0x00400000u)  // 2^-127, subnormal
                                    : __uint_as_float(byte << 23);
   typedef typename Elem<DT>::type T;
-  typedef T v4 __attribute__((ext_vector_type(4)));
-  v4 lo, hi;
+  constexpr int N = 16 / sizeof(T);  // values of a 16-byte store
+  typedef T vec __attribute__((ext_vector_type(N)));
+  vec* p = reinterpret_cast<vec*>(static_cast<T*>(y) + row * ldy + i);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    lo[j] = (T)mx_value((w >> (4 * j)) & 15u, scale);
-    hi[j] = (T)mx_value((w >> (4 * j + 16)) & 15u, scale);
+  for (int h = 0; h < 8 / N; ++h) {
+    vec v;
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = (T)mx_value((w >> (4 * (h * N + j))) & 15u, scale);
+    p[h] = v;
   }
-  v4* p = reinterpret_cast<v4*>(static_cast<T*>(y) + row * ldy + i);
-  p[0] = lo;
-  p[1] = hi;
 }
 
 // Rows that follow each other without a gap are one row, as long as its workgroups of 2048 values
