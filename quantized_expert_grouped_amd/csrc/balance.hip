@@ -2,17 +2,19 @@
 // token t's E logits, n the valid tokens, c[e] how many of their K routes each went to expert e:
 //   f[e] = c[e] / (n K),   P[e] = (1/n) sum_t p[t, e],   loss = E sum_e f[e] P[e],
 //   d loss / d logits[t, j] = (E / n) p[t, j] (f[j] - sum_e f[e] p[t, e]),
-// the counts being constants of the gradient.  Since sum_e p[t, e] = 1, f may be replaced by
-// f - 1/E in the bracket, and is: near balance f is almost constant and the bracket a small
-// difference of large terms otherwise.  f[e] - 1/E = (c[e] E - N) / (E n K), N = sum c, exact integers
-// up to one rounding.
+// the counts being constants of the gradient.  Since sum_e p[t, e] = 1, f may be replaced by its
+// difference from its mean in the bracket, and is: near balance f is almost constant and the bracket
+// a small difference of large terms otherwise.  f[e] - mean = (c[e] E - N) / (E n K), N = sum c:
+// exact integers up to one rounding.
 //
-// A row of logits is one wavefront's, read once into registers (-inf: an expert that the token may not
-// take; a row of nothing else has p = 0).  Forward: each workgroup keeps its rows' sums of p per
-// column in registers and its counts in LDS and leaves one row of partial sums; a second launch adds
-// those in a fixed order, so results do not change from run to run, and its last workgroup (an integer ticket)
-// forms the loss.
+// A row of logits is one wavefront's, read once into registers, the next row's loads under way
+// meanwhile (-inf: an expert that the token may not take; a row of nothing else has p = 0).  Forward:
+// each workgroup keeps its rows' sums of p per column in registers and its counts in LDS and leaves
+// one row of partial sums; a second launch adds those, and its last workgroup (an integer ticket)
+// forms the loss.  All float sums are in an order that depends on the sizes alone.
 #include <math.h>
+
+#include <type_traits>
 
 #include "common.hpp"
 #include "mx.hpp"
@@ -21,75 +23,129 @@ namespace moe {
 
 namespace {
 
-constexpr int kWaves = 16;  // wavefronts of a forward workgroup
+constexpr int kWaves = 16;             // wavefronts of a workgroup
+constexpr int kBackwardGroups = 256;   // one to a CU
 
-// Workspace: ticket, then per workgroup valid tokens, counts [E], sums [E].
+// Workspace: ticket, each joining workgroup's part of the loss, then per workgroup valid tokens,
+// counts [E], sums [E].
 struct Partials {
   int32_t* ticket;
-  int32_t* tokens;  // [groups]
+  float* loss;      // [kMaxJoins]
+  int32_t* tokens;  // [kBalanceGroups]
   int32_t* counts;  // [groups x E]
   float* sums;      // [groups x E]
 };
-__host__ __device__ inline Partials partials(void* ws, int groups, int E) {
+constexpr int kJoinCols = 32, kMaxJoins = 64;
+static_assert((1 + kMaxJoins + kBalanceGroups) * 4 <= kBalanceHeader, "header");
+__device__ __forceinline__ Partials partials(void* ws, int groups, int E) {
   Partials q;
   q.ticket = static_cast<int32_t*>(ws);
-  q.tokens = q.ticket + 64;
-  q.counts = q.tokens + kBalanceGroups;
+  q.loss = reinterpret_cast<float*>(q.ticket + 1);
+  q.tokens = q.ticket + 1 + kMaxJoins;
+  q.counts = q.ticket + kBalanceHeader / 4;
   q.sums = reinterpret_cast<float*>(q.counts + (size_t)groups * E);
   return q;
 }
 
+// The wavefront's largest value, or sum: DPP steps leave each row of 16 lanes with its row's, then the
+// four rows' are read into scalars.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+template <class F>
+__device__ __forceinline__ float wave_reduce(float v, F f) {
+  v = f(v, dpp<0xB1>(v));   // quad_perm [1, 0, 3, 2]
+  v = f(v, dpp<0x4E>(v));   // quad_perm [2, 3, 0, 1]
+  v = f(v, dpp<0x141>(v));  // lane i <-> 7 - i within each half row
+  v = f(v, dpp<0x140>(v));  // lane i <-> 15 - i within each row
+  auto row = [&](int i) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16 * i));
+  };
+  return f(f(row(0), row(1)), f(row(2), row(3)));
+}
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+  return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  return wave_reduce(v, [](float a, float b) { return a + b; });
 }
 
-// Lane l's columns of a row are j * 64 + l, j < VPL.  Gives exp(x - max) and 1 / their sum, 0 for a row
-// with nothing above -inf.
-template <int DT, int VPL>
-__device__ __forceinline__ float row_softmax(const void* logits, int64_t at, int E, float (&p)[VPL]) {
+// A lane's VPL columns of a row: VEC neighbours, then VEC neighbours 64 VEC further on, ...
+template <int VEC>
+__device__ __forceinline__ int column(int j, int lane) {
+  return (j / VEC * 64 + lane) * VEC + j % VEC;
+}
+
+template <int DT, int VPL, int VEC>
+struct Row {
   typedef typename Elem<DT>::type T;
-  const int lane = threadIdx.x & 63;
-  const T* l = static_cast<const T*>(logits) + at;
-  float m = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int c = j * 64 + lane;
-    p[j] = c < E ? (float)l[c] : -INFINITY;
-    m = fmaxf(m, p[j]);
-  }
-  m = wave_max(m);
-  if (m == -INFINITY) {
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) p[j] = 0.0f;
-    return 0.0f;
-  }
-  float s = 0.0f;
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    p[j] = expf(p[j] - m);
-    s += p[j];
-  }
-  return 1.0f / wave_sum(s);
-}
+  typedef T vec __attribute__((ext_vector_type(VEC)));
+  vec v[VPL / VEC];
 
-template <int DT, int VPL>
+  // columns past E stay at -inf: load leaves them alone
+  __device__ __forceinline__ Row() {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) v[j / VEC][j % VEC] = (T)-INFINITY;
+  }
+  // E is a multiple of VEC and the row VEC-aligned
+  __device__ __forceinline__ void load(const void* logits, int64_t at, int E, int lane) {
+    const T* l = static_cast<const T*>(logits) + at;
+#pragma unroll
+    for (int i = 0; i < VPL / VEC; ++i) {
+      const int c = column<VEC>(i * VEC, lane);
+      if (c < E) v[i] = *reinterpret_cast<const vec*>(l + c);
+    }
+  }
+  // exp(x - max) of each column, 0 past E; returns 1 / their sum, or 0 for a row with nothing above
+  // -inf.  The exponential is the hardware's 2^t of t = (x - max) log2 e: the roundings of the
+  // difference, the product and the constant make |x - max| 2.25 * 2^-24 of it, besides its ulp.
+  // (With expf the kernels were bound by its instructions.)
+  __device__ __forceinline__ float softmax(float (&p)[VPL]) const {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      p[j] = (float)v[j / VEC][j % VEC];
+      m = fmaxf(m, p[j]);
+    }
+    m = wave_max(m);
+    const bool none = m == -INFINITY;
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      p[j] = none ? 0.0f : __builtin_amdgcn_exp2f((p[j] - m) * 1.44269504088896341f);
+      s += p[j];
+    }
+    return none ? 0.0f : __builtin_amdgcn_rcpf(wave_sum(s));
+  }
+};
+
+template <int DT, int VPL, int VEC>
 __global__ __launch_bounds__(kWaves * 64) void balance_rows_kernel(BalanceArgs a, void* ws) {
-  __shared__ int32_t hist[VPL * 64];
-  __shared__ float sums[VPL * 64];
+  constexpr int kCols = VPL * 64;
+  __shared__ int32_t hist[kCols];
+  __shared__ float half[kWaves / 2][kCols];
   __shared__ int32_t tokens;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const Partials q = partials(ws, gridDim.x, a.E);
-  for (int e = threadIdx.x; e < VPL * 64; e += kWaves * 64) {
-    hist[e] = 0;
-    sums[e] = 0.0f;
-  }
+  const int64_t step = (int64_t)gridDim.x * kWaves;
+  int64_t t = (int64_t)blockIdx.x * kWaves + wave;
+  // the first row from t on that is valid (uniform)
+  auto valid_from = [&](int64_t u) {
+    while (u < a.T && a.valid && a.valid[u] == 0) u += step;
+    return u;
+  };
+  Row<DT, VPL, VEC> row;
+  int32_t id = -1;
+  auto fetch = [&]() {
+    if (t < a.T) {
+      row.load(a.logits, t * a.ld, a.E, lane);
+      if (lane < a.K) id = a.idx[t * a.K + lane];
+    }
+  };
+  t = valid_from(t);
+  fetch();
+  for (int e = threadIdx.x; e < kCols; e += kWaves * 64) hist[e] = 0;
   if (threadIdx.x == 0) {
     tokens = 0;
     if (blockIdx.x == 0) *q.ticket = 0;
@@ -99,170 +155,226 @@ __global__ __launch_bounds__(kWaves * 64) void balance_rows_kernel(BalanceArgs a
 #pragma unroll
   for (int j = 0; j < VPL; ++j) acc[j] = 0.0f;
   int mine = 0;
-  for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < a.T; t += (int64_t)gridDim.x * kWaves) {
-    if (a.valid && a.valid[t] == 0) continue;  // uniform
+  while (t < a.T) {
+    const Row<DT, VPL, VEC> now = row;
+    const int32_t e = id;
+    t = valid_from(t + step);
+    fetch();
     ++mine;
-    if (lane < a.K) {
-      const int e = a.idx[t * a.K + lane];
-      if (e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
-    }
+    if (lane < a.K && e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
     float p[VPL];
-    const float r = row_softmax<DT, VPL>(a.logits, t * a.ld, a.E, p);
+    const float r = now.softmax(p);
 #pragma unroll
     for (int j = 0; j < VPL; ++j) acc[j] = fmaf(p[j], r, acc[j]);
   }
   if (lane == 0 && mine) atomicAdd(&tokens, mine);
-  for (int wv = 0; wv < kWaves; ++wv) {  // in the wavefronts' order
-    if (wave == wv)
+  // the wavefronts' sums, the upper half onto the lower until one is left
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) sums[j * 64 + lane] += acc[j];
+  for (int n = kWaves / 2; n >= 1; n /= 2) {
+    if (wave >= n && wave < 2 * n)
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) half[wave - n][j * 64 + lane] = acc[j];
+    __syncthreads();
+    if (wave < n)
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) acc[j] += half[wave][j * 64 + lane];
     __syncthreads();
   }
-  for (int e = threadIdx.x; e < a.E; e += kWaves * 64) {
+  if (wave == 0)
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const int c = column<VEC>(j, lane);
+      if (c < a.E) q.sums[(size_t)blockIdx.x * a.E + c] = acc[j];
+    }
+  for (int e = threadIdx.x; e < a.E; e += kWaves * 64)
     q.counts[(size_t)blockIdx.x * a.E + e] = hist[e];
-    q.sums[(size_t)blockIdx.x * a.E + e] = sums[e];
-  }
   if (threadIdx.x == 0) q.tokens[blockIdx.x] = tokens;
 }
 
-// 32 columns by 8 strands of workgroups' partial rows.
-__global__ __launch_bounds__(256) void balance_join_kernel(int E, int K, int groups, void* ws,
-                                                           int32_t* __restrict__ counts,
-                                                           float* __restrict__ prob_mean,
-                                                           float* __restrict__ loss) {
-  __shared__ int32_t c8[8][32];
-  __shared__ float s8[8][32];
-  __shared__ int32_t n4[4];
-  __shared__ bool last;
+// 32 columns by 32 strands of workgroups' partial rows, 8 of them each, all loads under way at once.
+__global__ __launch_bounds__(1024) void balance_join_kernel(int E, int K, int groups, void* ws,
+                                                            int32_t* __restrict__ counts,
+                                                            float* __restrict__ prob_mean,
+                                                            float* __restrict__ loss) {
+  constexpr int kStrands = 32;
+  static_assert(kBalanceGroups == 8 * kStrands, "8 rows a strand");
+  __shared__ int32_t cs[16][kJoinCols];
+  __shared__ float ss[16][kJoinCols];
+  __shared__ int32_t ns[4];
   const Partials q = partials(ws, groups, E);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = threadIdx.x & 31, strand = threadIdx.x >> 5;
-  const int e = blockIdx.x * 32 + col;
-  int n = threadIdx.x < groups ? q.tokens[threadIdx.x] : 0;
+  const int e = blockIdx.x * kJoinCols + col;
+  int32_t c8[8];
+  float s8[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int g = strand + kStrands * i;
+    const bool on = g < groups && e < E;
+    c8[i] = on ? q.counts[(size_t)g * E + e] : 0;
+    s8[i] = on ? q.sums[(size_t)g * E + e] : 0.0f;
+  }
+  int n = threadIdx.x < groups ? q.tokens[threadIdx.x] : 0;  // the first 256 threads
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o);
-  if ((threadIdx.x & 63) == 0) n4[threadIdx.x >> 6] = n;
-  int32_t c = 0;
-  float s = 0.0f;
-  if (e < E)
-    for (int g = strand; g < groups; g += 8) {
-      c += q.counts[(size_t)g * E + e];
-      s += q.sums[(size_t)g * E + e];
-    }
-  c8[strand][col] = c;
-  s8[strand][col] = s;
+  if (lane == 0 && wave < 4) ns[wave] = n;
+  int32_t c = ((c8[0] + c8[1]) + (c8[2] + c8[3])) + ((c8[4] + c8[5]) + (c8[6] + c8[7]));
+  float s = ((s8[0] + s8[1]) + (s8[2] + s8[3])) + ((s8[4] + s8[5]) + (s8[6] + s8[7]));
+  c += __shfl_xor(c, 32);  // the wavefront's two strands
+  s += __shfl_xor(s, 32);
+  if (lane < 32) {
+    cs[wave][col] = c;
+    ss[wave][col] = s;
+  }
   __syncthreads();
-  n = n4[0] + n4[1] + n4[2] + n4[3];
-  if (strand == 0 && e < E) {
+  n = (ns[0] + ns[1]) + (ns[2] + ns[3]);
+  if (wave == 0) {
+    c = 0;
+    s = 0.0f;
+    if (lane < 32)
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-      c += c8[i][col];
-      s += s8[i][col];
+      for (int w = 0; w < 16; ++w) {
+        c += cs[w][col];
+        s += ss[w][col];
+      }
+    const float mean = n > 0 ? s / (float)n : 0.0f;
+    if (lane < 32 && e < E) {
+      counts[e] = c;
+      prob_mean[e] = mean;
     }
-    counts[e] = c;
-    prob_mean[e] = n > 0 ? s / (float)n : 0.0f;
+    const float part = wave_sum((float)c * mean);  // 0 in lanes without a column
+    int before = 0;
+    if (lane == 0) {
+      if (blockIdx.x == 0) counts[E] = n;
+      __hip_atomic_store(q.loss + blockIdx.x, part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      before = __hip_atomic_fetch_add(q.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (__builtin_amdgcn_readfirstlane(before) != (int)gridDim.x - 1) return;
+    const float v = lane < (int)gridDim.x ? __hip_atomic_load(q.loss + lane, __ATOMIC_RELAXED,
+                                                              __HIP_MEMORY_SCOPE_AGENT)
+                                          : 0.0f;
+    const float sum = wave_sum(v);
+    if (lane == 0) *loss = n > 0 ? sum * ((float)E / ((float)n * (float)K)) : 0.0f;
   }
-  if (threadIdx.x == 0 && blockIdx.x == 0) counts[E] = n;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(q.ticket, 1) == (int)gridDim.x - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  // loss = E sum_e f[e] P[e]: 256 strands of columns, then a tree, a fixed order
-  float v = 0.0f;
-  for (int i = threadIdx.x; i < E; i += 256) {
-    const int32_t ci = __hip_atomic_load(counts + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const float pi = __hip_atomic_load(prob_mean + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    v = fmaf((float)ci, pi, v);
-  }
-  v = wave_sum(v);
-  __shared__ float v4[4];
-  if ((threadIdx.x & 63) == 0) v4[threadIdx.x >> 6] = v;
-  __syncthreads();
-  if (threadIdx.x == 0)
-    *loss = n > 0 ? ((v4[0] + v4[1]) + (v4[2] + v4[3])) * ((float)E / ((float)n * (float)K)) : 0.0f;
 }
 
-template <int DT, int VPL>
-__global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs a,
-                                                               const int32_t* __restrict__ counts,
-                                                               const float* __restrict__ grad_loss,
-                                                               void* __restrict__ grad,
-                                                               int64_t ld_grad) {
-  typedef typename Elem<DT>::type T;
+template <int DT, int VPL, int VEC>
+__global__ __launch_bounds__(kWaves * 64) void balance_backward_kernel(
+    BalanceArgs a, const int32_t* __restrict__ counts, const float* __restrict__ grad_loss,
+    void* __restrict__ grad, int64_t ld_grad) {
+  typedef Row<DT, VPL, VEC> R;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t step = (int64_t)gridDim.x * kWaves;
+  int64_t t = (int64_t)blockIdx.x * kWaves + wave;
+  R row;
+  bool on = false;
+  auto fetch = [&]() {
+    on = t < a.T && (!a.valid || a.valid[t] != 0);  // uniform
+    if (on) row.load(a.logits, t * a.ld, a.E, lane);
+  };
+  fetch();
   const int n = counts[a.E];
-  float dev[VPL];
-  int64_t total = 0;
   int32_t c[VPL];
+  int64_t total = 0;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    const int e = j * 64 + lane;
-    c[j] = e < a.E ? counts[e] : 0;
+    c[j] = 0;
+    if (column<VEC>(j, lane) < a.E) c[j] = counts[column<VEC>(j, lane)];
     total += c[j];
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o);
-  // (E / n) (f - 1/E) = (c E - N) / (n n K)
+  // g (E / n) (f - mean) = g (c E - N) / (n n K)
   const float nf = (float)n;
-  const float scale = n > 0 ? (grad_loss ? *grad_loss : 1.0f) / (nf * (float)a.K) / nf : 0.0f;
+  const float scale =
+      n > 0 ? (grad_loss ? *grad_loss : 1.0f) / (nf * (float)a.K) / nf : 0.0f;
+  float dev[VPL];
 #pragma unroll
   for (int j = 0; j < VPL; ++j) dev[j] = (float)((int64_t)c[j] * a.E - total) * scale;
-  for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < a.T; t += (int64_t)gridDim.x * 4) {
-    T* g = static_cast<T*>(grad) + t * ld_grad;
-    float p[VPL];
-    float r = 0.0f, dot = 0.0f;
-    const bool on = !a.valid || a.valid[t] != 0;  // uniform
-    if (on) {
-      r = row_softmax<DT, VPL>(a.logits, t * a.ld, a.E, p);
+  while (t < a.T) {
+    const R now = row;
+    const bool live = on;
+    typename R::T* g = static_cast<typename R::T*>(grad) + t * ld_grad;
+    t += step;
+    fetch();
+    float p[VPL], r = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) p[j] = 0.0f;
+    if (live) {
+      r = now.softmax(p);
 #pragma unroll
       for (int j = 0; j < VPL; ++j) dot = fmaf(p[j], dev[j], dot);
       dot = wave_sum(dot) * r;
     }
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const int e = j * 64 + lane;
-      if (e < a.E) g[e] = on ? (T)(p[j] * r * (dev[j] - dot)) : (T)0.0f;
+    for (int i = 0; i < VPL / VEC; ++i) {
+      const int e = column<VEC>(i * VEC, lane);
+      typename R::vec v;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        v[j] = (typename R::T)(live ? p[i * VEC + j] * r * (dev[i * VEC + j] - dot) : 0.0f);
+      if (e < a.E) *reinterpret_cast<typename R::vec*>(g + e) = v;
     }
   }
 }
 
+// VEC values of a row are loaded together, 16 bytes at most, where E and every row's address allow
+// it (at E = 512 in bf16 the forward pass takes 34 us for 30118 rows with single values).
+template <int DT, class F>
+hipError_t dispatch(int E, bool together, F f) {
+  constexpr int kMost = DT == kF32 ? 4 : 8;
+  const int vpl = (E + 63) / 64;
+  auto go = [&](auto V) {
+    constexpr int VPL = decltype(V)::value;
+    constexpr int VEC = VPL < kMost ? VPL : kMost;
+    if (together && E % VEC == 0)
+      f(V, std::integral_constant<int, VEC>{});
+    else
+      f(V, std::integral_constant<int, 1>{});
+    return hipGetLastError();
+  };
+  return vpl <= 1    ? go(std::integral_constant<int, 1>{})
+         : vpl <= 2  ? go(std::integral_constant<int, 2>{})
+         : vpl <= 4  ? go(std::integral_constant<int, 4>{})
+         : vpl <= 8  ? go(std::integral_constant<int, 8>{})
+         : vpl <= 16 ? go(std::integral_constant<int, 16>{})
+                     : go(std::integral_constant<int, 32>{});
+}
+
+// Whether every row of a matrix starts at a 16-byte boundary.
+bool rows_aligned(const void* p, int64_t ld, int dtype) {
+  return (uintptr_t)p % 16 == 0 && ld * (dtype == kF32 ? 4 : 2) % 16 == 0;
+}
+
 template <int DT>
-hipError_t forward(const BalanceArgs& a, int groups, void* ws, hipStream_t s) {
-  const int vpl = (a.E + 63) / 64;
-  if (vpl <= 1) balance_rows_kernel<DT, 1><<<groups, kWaves * 64, 0, s>>>(a, ws);
-  else if (vpl <= 2) balance_rows_kernel<DT, 2><<<groups, kWaves * 64, 0, s>>>(a, ws);
-  else if (vpl <= 4) balance_rows_kernel<DT, 4><<<groups, kWaves * 64, 0, s>>>(a, ws);
-  else if (vpl <= 8) balance_rows_kernel<DT, 8><<<groups, kWaves * 64, 0, s>>>(a, ws);
-  else if (vpl <= 16) balance_rows_kernel<DT, 16><<<groups, kWaves * 64, 0, s>>>(a, ws);
-  else balance_rows_kernel<DT, 32><<<groups, kWaves * 64, 0, s>>>(a, ws);
-  return hipGetLastError();
+hipError_t forward(const BalanceArgs& a, void* ws, hipStream_t s) {
+  return dispatch<DT>(a.E, rows_aligned(a.logits, a.ld, a.dtype), [&](auto V, auto W) {
+    balance_rows_kernel<DT, decltype(V)::value, decltype(W)::value>
+        <<<balance_groups(a.T), kWaves * 64, 0, s>>>(a, ws);
+  });
 }
 
 template <int DT>
 hipError_t backward(const BalanceArgs& a, const int32_t* counts, const float* grad_loss, void* grad,
                     int64_t ld, hipStream_t s) {
-  const int vpl = (a.E + 63) / 64;
-  const int grid = a.T / 4 + 1 < 2048 ? a.T / 4 + 1 : 2048;
-  if (vpl <= 1) balance_backward_kernel<DT, 1><<<grid, 256, 0, s>>>(a, counts, grad_loss, grad, ld);
-  else if (vpl <= 2) balance_backward_kernel<DT, 2><<<grid, 256, 0, s>>>(a, counts, grad_loss, grad, ld);
-  else if (vpl <= 4) balance_backward_kernel<DT, 4><<<grid, 256, 0, s>>>(a, counts, grad_loss, grad, ld);
-  else if (vpl <= 8) balance_backward_kernel<DT, 8><<<grid, 256, 0, s>>>(a, counts, grad_loss, grad, ld);
-  else if (vpl <= 16) balance_backward_kernel<DT, 16><<<grid, 256, 0, s>>>(a, counts, grad_loss, grad, ld);
-  else balance_backward_kernel<DT, 32><<<grid, 256, 0, s>>>(a, counts, grad_loss, grad, ld);
-  return hipGetLastError();
+  const bool together = rows_aligned(a.logits, a.ld, a.dtype) && rows_aligned(grad, ld, a.dtype);
+  const int groups = (a.T + kWaves - 1) / kWaves;
+  return dispatch<DT>(a.E, together, [&](auto V, auto W) {
+    balance_backward_kernel<DT, decltype(V)::value, decltype(W)::value>
+        <<<groups < kBackwardGroups ? groups : kBackwardGroups, kWaves * 64, 0, s>>>(a, counts, grad_loss, grad, ld);
+  });
 }
 
 }  // namespace
 
 hipError_t launch_balance_loss(const BalanceArgs& a, int32_t* counts, float* prob_mean, float* loss,
                                void* ws, hipStream_t s) {
-  const int groups = balance_groups(a.T);
-  hipError_t e = a.dtype == kF32    ? forward<kF32>(a, groups, ws, s)
-                 : a.dtype == kBF16 ? forward<kBF16>(a, groups, ws, s)
-                                    : forward<kF16>(a, groups, ws, s);
+  hipError_t e = a.dtype == kF32    ? forward<kF32>(a, ws, s)
+                 : a.dtype == kBF16 ? forward<kBF16>(a, ws, s)
+                                    : forward<kF16>(a, ws, s);
   if (e != hipSuccess) return e;
-  balance_join_kernel<<<(a.E + 31) / 32, 256, 0, s>>>(a.E, a.K, groups, ws, counts, prob_mean, loss);
+  balance_join_kernel<<<(a.E + kJoinCols - 1) / kJoinCols, 1024, 0, s>>>(
+      a.E, a.K, balance_groups(a.T), ws, counts, prob_mean, loss);
   return hipGetLastError();
 }
 

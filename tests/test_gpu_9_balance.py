@@ -53,12 +53,13 @@ def check(xt, idx, v, dtype, g, got):
     counts, prob, loss, grad, p, f = mxref.balance(x, idx, v)
     n = max(int(counts[E]), 1)
     assert np.array_equal(host(got[0]), counts)
-    # a probability: exp of an exact-to-rounding difference d (relative error |d| 2^-24) within 2 ulp, the
+    # a probability: 2^t within 2 ulp, t = d log2 e of a rounded difference d by a rounded constant (each a
+    # relative 2^-24 of t at most, the constant's a quarter of that: 2.25 |d| 2^-24 of the power), the
     # sum of E terms over a lane's E / 64 and 6 steps across lanes, the quotient, the product
     on = np.ones(T, bool) if v is None else v != 0
     fin = np.isfinite(x) & on[:, None]
     d = np.where(fin, np.where(fin, x, -1e300).max(1, keepdims=True) - np.where(fin, x, 0.0), 0.0)
-    eps = (np.minimum(d, 150) + E / 64 + 16) * 2.0 ** -24
+    eps = (2.25 * np.minimum(d, 150) + E / 64 + 16) * 2.0 ** -24
     eps = eps + (p * eps).sum(1, keepdims=True)      # the sum's own terms carry theirs
     tiny = 2.0 ** -126                               # smaller exponentials may be flushed
     dp = p * eps + tiny
