@@ -191,11 +191,12 @@ __device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t
 
 // A workgroup's tile: BN weight rows by BM routed rows, its wavefronts in WN slices of the columns by WM of
 // the rows, each wavefront TN x TM MFMA tiles; row tiles are dealt to the WM in turn, so that few
-// rows still keep all busy.  A stage is 256 values of K, 128 bytes of each row.
+// rows still keep all busy.  A stage is 256 values of K, 128 bytes of each row, in one of NBUF
+// buffers.
 constexpr int kStage = 128;
-template <int WN_, int WM_, int TN_, int TM_, int MINW_>
+template <int WN_, int WM_, int TN_, int TM_, int NBUF_, int MINW_>
 struct Geo {
-  static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_;
+  static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_, NBUF = NBUF_;
   static constexpr int kMinWaves = MINW_;  // wavefronts to fit on a SIMD
   static constexpr int kWaves = WN * WM;
   static constexpr int BN = WN * TN * 32, BM = WM * TM * 32, kRows = BN + BM;
@@ -211,8 +212,8 @@ struct Geo {
 };
 template <class G>
 struct Lds {
-  uint8_t rows[G::kBuf];          // a stage's weight rows, then its routed rows
-  uint8_t scales[G::kRows * 16];  // their scale bytes: of 512 values, or of a stage
+  uint8_t rows[G::NBUF][G::kBuf];          // a stage's weight rows, then its routed rows
+  uint8_t scales[G::NBUF][G::kRows * 16];  // their scale bytes: of 512 values, or of a stage
 };
 
 // Where a row's 16-byte piece c lies among its 8 in LDS: at c ^ swizzle(row).  Lanes of consecutive
@@ -276,24 +277,23 @@ __device__ __forceinline__ void plan_rows(Dma<G, WIDE>& d, int k_in, AR arow, in
   }
 }
 
-// A stage's rows to LDS at `rows`, scale bytes from a stage on to `scales`.  `last_half`: of a last stage of 128 values, whose pieces 4..7 (scale
-// bytes 4..7) do not exist; those lanes load the first ones again, and the products leave them out.
+// Load i of a stage's rows to LDS at `rows`, weight rows first; a stage's scale bytes to `scales`.
+// `last_half`: of a last stage of 128 values, whose pieces 4..7 (scale bytes 4..7) do not exist; those
+// lanes load the first ones again, and the products leave them out.
 template <class G, bool WIDE>
-__device__ __forceinline__ void issue_rows(const Dma<G, WIDE>& d, int stage, uint32_t rows, bool last_half, int wave, int lane) {
+__device__ __forceinline__ void issue_row(const Dma<G, WIDE>& d, int i, int stage, uint32_t rows, bool last_half,
+                                          int wave, int lane) {
   const size_t k = (size_t)stage * kStage;
   auto off = [&](uint32_t o, int row) {
     if (WIDE || !last_half) return o;
     return o - ((((lane & 7) ^ swizzle(row)) & 4) ? 64u : 0u);
   };
-#pragma unroll
-  for (int i = 0; i < G::kWI; ++i) {
+  if (i < G::kWI) {
     const int l = min(wave + G::kWaves * i, G::kW - 1);
     dma16(d.w + k, off(d.wo[i], 8 * l + lane / 8), rows + 1024 * l);
-  }
-#pragma unroll
-  for (int i = 0; i < G::kAI; ++i) {
-    const int l = min(wave + G::kWaves * i, G::kA - 1);
-    dma16(d.a + k, off(d.ao[i], 8 * l + lane / 8), rows + G::BN * kStage + 1024 * l);
+  } else {
+    const int j = i - G::kWI, l = min(wave + G::kWaves * j, G::kA - 1);
+    dma16(d.a + k, off(d.ao[j], 8 * l + lane / 8), rows + G::BN * kStage + 1024 * l);
   }
 }
 template <class G, bool WIDE>
@@ -322,22 +322,30 @@ __device__ __forceinline__ Reads plan_reads(const Lds<G>& lds, int wn, int wm, i
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const int at = l32 * kStage + 16 * ((4 * half + s) ^ sz);
-    r.w[s] = lds.rows + wn * G::TN * 32 * kStage + at;
-    r.a[s] = lds.rows + (G::BN + wm * 32) * kStage + at;
+    r.w[s] = lds.rows[0] + wn * G::TN * 32 * kStage + at;
+    r.a[s] = lds.rows[0] + (G::BN + wm * 32) * kStage + at;
   }
-  r.sw = lds.scales + (wn * G::TN * 32 + l32) * kStride + 4 * half;
-  r.sa = lds.scales + (G::BN + wm * 32 + l32) * kStride + 4 * half;
+  r.sw = lds.scales[0] + (wn * G::TN * 32 + l32) * kStride + 4 * half;
+  r.sa = lds.scales[0] + (G::BN + wm * 32 + l32) * kStride + 4 * half;
   return r;
 }
 
-// The wavefront's products of one stage, with NL of its TM row tiles holding rows; scales_at: the
-// stage's place among its row's scale bytes.
-template <class G, bool WIDE, int NL>
-__device__ __forceinline__ void products(const Reads& r, int scales_at, v16f (&acc)[G::TN][G::TM],
-                                         bool last_half, int lane) {
+// The wavefront's products of one stage, with NL of its TM row tiles holding rows.  rows_at: the stage's
+// buffer; scales_at: its set of scale bytes and place among its row's.  A wavefront that issues a load to LDS
+// waits until the CU has taken it, about 200 clocks while all issue (a fifth to a half of a stage's
+// time if it issues them in a row), so load(i), i < LOADS, are spread over the products, which go on meanwhile.
+template <class G, bool WIDE, int NL, int LOADS, class F>
+__device__ __forceinline__ void products(const Reads& r, int rows_at, int scales_at, v16f (&acc)[G::TN][G::TM],
+                                         bool last_half, int lane, F load) {
   constexpr int kStride = WIDE ? 16 : 8;
+  constexpr int N = NL > 0 ? NL : 1;
   const bool none = !WIDE && last_half && lane >= 32;  // this lane's blocks do not exist: codes 0 at scale 1
-  int sw[G::TN], sa[NL > 0 ? NL : 1];
+  if constexpr (NL == 0) {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) load(i);
+    return;
+  }
+  int sw[G::TN], sa[N];
 #pragma unroll
   for (int j = 0; j < G::TN; ++j) {
     sw[j] = *reinterpret_cast<const int*>(r.sw + scales_at + j * 32 * kStride);
@@ -348,22 +356,41 @@ __device__ __forceinline__ void products(const Reads& r, int scales_at, v16f (&a
     sa[i] = *reinterpret_cast<const int*>(r.sa + scales_at + i * G::WM * 32 * kStride);
     if (!WIDE) sa[i] = none ? 0x7f7f7f7f : sa[i];
   }
-  auto step = [&](auto S) {
-    constexpr int s = decltype(S)::value;
-    v4i w[G::TN], a[NL > 0 ? NL : 1];
+  struct Operands {
+    v4i w[G::TN], a[N];
+  };
+  auto read = [&](int s) {
+    Operands o;
 #pragma unroll
     for (int j = 0; j < G::TN; ++j) {
-      w[j] = *reinterpret_cast<const v4i*>(r.w[s] + j * 32 * kStage);
+      o.w[j] = *reinterpret_cast<const v4i*>(r.w[s] + rows_at + j * 32 * kStage);
       if (!WIDE)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) w[j][q] = none ? 0 : w[j][q];
+        for (int q = 0; q < 4; ++q) o.w[j][q] = none ? 0 : o.w[j][q];
     }
 #pragma unroll
-    for (int i = 0; i < NL; ++i) a[i] = *reinterpret_cast<const v4i*>(r.a[s] + i * G::WM * 32 * kStage);
+    for (int i = 0; i < NL; ++i) o.a[i] = *reinterpret_cast<const v4i*>(r.a[s] + rows_at + i * G::WM * 32 * kStage);
+    return o;
+  };
+  constexpr int kSpread = 2 * N * G::TN;  // over the first half of them: they have to land by the next stage
+  Operands now = read(0);
+  auto step = [&](auto S) {
+    constexpr int s = decltype(S)::value;
+    Operands next = now;
+    if (s < 3) next = read(s + 1);
 #pragma unroll
     for (int i = 0; i < NL; ++i)
 #pragma unroll
-      for (int j = 0; j < G::TN; ++j) acc[j][i] = mfma_mx<s>(w[j], a[i], acc[j][i], sw[j], sa[i]);
+      for (int j = 0; j < G::TN; ++j) {
+        acc[j][i] = mfma_mx<s>(now.w[j], now.a[i], acc[j][i], sw[j], sa[i]);
+        const int m = (s * NL + i) * G::TN + j;
+        if (LOADS > 0 && m <= kSpread) {
+#pragma unroll
+          for (int l = m * LOADS / kSpread; l < (m + 1) * LOADS / kSpread && l < LOADS; ++l) load(l);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    now = next;
   };
   step(std::integral_constant<int, 0>{});
   step(std::integral_constant<int, 1>{});
@@ -441,29 +468,66 @@ __device__ __forceinline__ void store_tile(const MxProblem& p, const v16f (&acc)
   }
 }
 
-// The tile's products along K.  `between` is called once a stage, with loads under way.
-template <class G, bool WIDE, int NL, class F>
-__device__ __forceinline__ void main_loop(const Reads& r, const Dma<G, WIDE>& d, uint32_t lrows, uint32_t lscales,
-                                          v16f (&acc)[G::TN][G::TM], int k_in, F between, int wave, int lane) {
+// Where the workgroup is in its buffers: the one at work, and the sets of scale bytes at work and last loaded.
+struct Ring {
+  int buf = 0, set = -1, loaded = -1;
+};
+
+template <class G, bool WIDE>
+__device__ __forceinline__ void issue_stage_scales(const Dma<G, WIDE>& d, int k, bool last_half, Ring& ring, uint32_t lscales,
+                                                   int wave, int lane) {
+  if (WIDE && (k & 1) != 0) return;
+  ring.loaded = (ring.loaded + 1) & (G::NBUF - 1);
+  issue_scales(d, k, lscales + ring.loaded * G::kRows * 16, last_half, wave, lane);
+}
+
+// The tile's products along K.  `between` is called once a stage.  With two buffers each stage's loads are issued
+// among the products of the one before it: its first stage's were before this, and its last stage
+// issues the first of the next tile, which `turn_over` puts in place of this one in d.
+template <class G, bool WIDE, int NL, class F, class A>
+__device__ __forceinline__ void main_loop(const Reads& r, Dma<G, WIDE>& d, Ring& ring, uint32_t lrows,
+                                          uint32_t lscales, v16f (&acc)[G::TN][G::TM], int k_in, F between, A turn_over,
+                                          int wave, int lane) {
+  constexpr int kLoads = G::kWI + G::kAI;
   const int stages = (k_in + 255) / 256;
+  auto half_stage = [&](int k) { return !WIDE && 256 * (k + 1) > k_in; };
   for (int k = 0; k < stages; ++k) {
-    const bool last_half = !WIDE && 256 * (k + 1) > k_in;
     wait_and_barrier();
-    if (!WIDE || (k & 1) == 0) issue_scales(d, k, lscales, last_half, wave, lane);
-    issue_rows(d, k, lrows, last_half, wave, lane);
-    between();
-    wait_and_barrier();
-    products<G, WIDE, NL>(r, WIDE ? (k & 1) * 8 : 0, acc, last_half, lane);
+    if constexpr (G::NBUF == 1) {
+      issue_stage_scales(d, k, half_stage(k), ring, lscales, wave, lane);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) issue_row(d, i, k, lrows, half_stage(k), wave, lane);
+      between();
+      wait_and_barrier();
+    }
+    if (!WIDE || (k & 1) == 0) ring.set = (ring.set + 1) & (G::NBUF - 1);
+    const int scales_at = ring.set * G::kRows * 16 + (WIDE ? (k & 1) * 8 : 0);
+    if constexpr (G::NBUF == 2) {
+      // after the products while other wavefronts' still go on; the largest tile has no registers for that
+      constexpr bool kAfter = G::TM <= 2;
+      if (!kAfter) between();
+      const int kn = k + 1 < stages ? k + 1 : 0;
+      if (kn == 0) turn_over();
+      issue_stage_scales(d, kn, half_stage(kn), ring, lscales, wave, lane);
+      products<G, WIDE, NL, kLoads>(r, ring.buf * G::kBuf, scales_at, acc, half_stage(k), lane, [&](int i) {
+        issue_row(d, i, kn, lrows + (ring.buf ^ 1) * G::kBuf, half_stage(kn), wave, lane);
+      });
+      if (kAfter) between();
+      if (k + 1 < stages) ring.buf ^= 1;
+    } else {
+      products<G, WIDE, NL, 0>(r, 0, scales_at, acc, half_stage(k), lane, [](int) {});
+    }
   }
 }
 
-// The lane's sum of v over the lanes up to it.
-__device__ __forceinline__ int scan(int v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int x = __shfl_up(v, o);
-    v += lane >= o ? x : 0;
-  }
+// The lane's sum of v over the lanes up to it: within rows of 16 lanes, then over the rows.
+__device__ __forceinline__ int scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
   return v;
 }
 
@@ -488,7 +552,7 @@ __global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kerne
     before += tiles_of(o - prev);
     prev = o;
   }
-  const int upto = scan(before, lane);
+  const int upto = scan(before);
   const uint32_t pairs = (uint32_t)__builtin_amdgcn_readlane(upto, 63) * n_tiles;
   before = upto - before;
 
@@ -521,7 +585,7 @@ __global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kerne
     } else if (at == 1) {
       const int o = min(piece, p.rows), n = max(__shfl_down(o, 1) - o, 0);
       const int mine = lane < seg && u.expert + lane < p.E ? tiles_of(n) : 0;
-      const int incl = scan(mine, lane);
+      const int incl = scan(mine);
       const int s = __popcll(ballot(incl <= u.row0));  // lanes all of whose tiles come before
       const int m = u.row0 - (__builtin_amdgcn_readlane(incl, s) - __builtin_amdgcn_readlane(mine, s));
       const int rows = __builtin_amdgcn_readlane(n, s), count = __builtin_amdgcn_readlane(mine, s);
@@ -563,11 +627,25 @@ __global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kerne
   asm volatile("" : "+s"(lrows), "+s"(lscales));
   const Reads r = plan_reads<G, WIDE>(lds, wn, wm, lane);
   while (at < 3) advance(pair);
+  Ring ring;
+  d = e;
+  if (G::NBUF == 2) {
+    const bool last_half = !WIDE && p.k_in < 256;
+    issue_stage_scales(d, 0, last_half, ring, lscales, wave, lane);
+#pragma unroll
+    for (int i = 0; i < G::kWI + G::kAI; ++i) issue_row(d, i, 0, lrows, last_half, wave, lane);
+  }
   for (;;) {
-    d = e, t = u, n0 = un0, at = 0;
+    t = u, n0 = un0, at = 0;
+    if (G::NBUF == 1) d = e;
     const uint32_t next = pair + step;
     auto between = [&]() {
       if (next < end) advance(next);
+    };
+    auto turn_over = [&]() {  // after the last pair its first stage is loaded once more, for nothing
+      if (next >= end) return;
+      while (at < 3) advance(next);
+      d = e;
     };
     const int row_tiles = (t.nrows + 31) / 32;
     const int live = row_tiles > wm ? (row_tiles - wm + G::WM - 1) / G::WM : 0;
@@ -582,7 +660,7 @@ __global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kerne
           for (int i = 0; i < NL; ++i)
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[j][i][q] = 0.0f;
-        main_loop<G, WIDE, NL>(r, d, lrows, lscales, acc, p.k_in, between, wave, lane);
+        main_loop<G, WIDE, NL>(r, d, ring, lrows, lscales, acc, p.k_in, between, turn_over, wave, lane);
         if (!kSwiglu) {  // tiles are turned in the stage's buffer once every wavefront is done with it
           asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
           __builtin_amdgcn_s_barrier();
@@ -592,7 +670,7 @@ __global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kerne
         for (int i = 0; i < NL; ++i) {
           const int r0 = __builtin_amdgcn_readfirstlane(here((i * G::WM + wm) * 32));
           store_tile<G, EPI>(p, acc, i, (size_t)t.row0 + r0, min(t.nrows - r0, 32), n0 + wn * (kFeat / G::WN),
-                             lds.rows + 4096 * wave, here(lane));
+                             lds.rows[ring.buf] + 4096 * wave, here(lane));
         }
       }
     };
@@ -600,11 +678,14 @@ __global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kerne
     go(std::integral_constant<int, 1>{});
     go(std::integral_constant<int, 2>{});
     go(std::integral_constant<int, 3>{});
-    static_assert(G::TM <= 3, "instances");
-    if (next >= end) return;
+    go(std::integral_constant<int, 4>{});
+    static_assert(G::TM <= 4, "instances");
+    if (next >= end) break;
     while (at < 3) advance(next);
+    if (G::NBUF == 2) ring.buf ^= 1;
     pair = next;
   }
+  if (G::NBUF == 2) wait_and_barrier();  // no load to LDS is under way when the workgroup ends
 }
 
 constexpr int kCus = 256;  // MI355X
@@ -642,36 +723,41 @@ hipError_t launch_wide_any(const MxProblem& p, hipStream_t s) {
 
 }  // namespace
 
-// Which kernel, by sizes alone (us, MI355X; "few" is the narrow kernel, then the wide one's tiles):
-//                                              few   256 x 64  128 x 192  256 x 128
+// Which kernel, by sizes alone (us, MI355X; columns: the narrow kernel, then the wide one's tiles, whose
+// last two have two buffers):
+//                                   narrow  256 x 64  128 x 192  256 x 256  128 x 128
 //   gate/up 2048 -> 2 x 512, 512 experts, K = 10
-//     1 token   (160 32 x 32 tiles)             7.0      11.8
-//     4 tokens  (640)                          13.8      15.0
-//     16 tokens (2560)                         39.6      33.6
-//     2048 tokens (40 rows an expert)           339       119        138        125
-//     8192 tokens (160 rows)                    900       205        183        213
-//     32768 tokens (640 rows)                  2995       622        588        534
+//     1 token                          7.0      11.8                              9.3
+//     4 tokens                        13.8      15.0                             14.3
+//     16 tokens                       39.6      35.6       34.9       40.1       34.8
+//     2048 tokens (40 rows each)       341       118        137        147        140
+//     8192 tokens (160 rows)           903       204        179        180        239
+//     32768 tokens (640 rows)         2994       644        578        480        597
+//   down 512 -> 2048, 512 experts, K = 10
+//     16 tokens                       23.1      19.4       22.5       26.0       24.4
+//     8192 tokens                      600       160        144        166        207
 //   one 4096 x 4096 matrix
-//     64 rows (256 tiles)                      14.6      20.3
-//     256 rows (1024 tiles)                    33.0      24.5
-//     1024 rows (128 pairs of 256 x 128)         99        30         32         34
-//     8191 rows                                 708       115        107         99
-// The narrow kernel wins while its workgroups all run at once, 3 to a CU; the smallest wide tile
-// while experts are short or the larger tiles would not fill the CUs twice.
+//     16 rows                          9.6      20.4       19.2       19.5       14.3
+//     256 rows                        33.2      24.5       23.3       31.3       17.5
+//     1024 rows                         99      29.2       31.6       31.6       21.1
+//     8191 rows                        707       112        112         88        112
+// The narrow kernel wins while its workgroups all run at once, 3 to a CU; 128 x 128 while larger
+// tiles would not fill the CUs twice; then the tile's height goes by the rows an expert has.
 hipError_t launch_mx_mm(const MxProblem& p_, hipStream_t s) {
   MxProblem p = p_;
   // n / K = n * k_mul >> k_shift for n < 2^30, K <= 64: k_mul K - 2^k_shift <= K <= 2^(k_shift - 30)
   p.k_shift = 30;
   while (1 << (p.k_shift - 30) < p.K) ++p.k_shift;
   p.k_mul = (uint32_t)(((uint64_t)1 << p.k_shift) / p.K + 1);
-  const int64_t tiles = std::min<int64_t>(p.rows, p.rows / 32 + p.E) * (p.n_out / 32);
-  if (tiles <= 3 * kCus) return launch_narrow(p, s);
+  auto tiles = [&](int high) { return std::min<int64_t>(p.rows, (int64_t)p.rows / high + p.E); };
+  if (tiles(32) * (p.n_out / 32) <= 3 * kCus) return launch_narrow(p, s);
   const int64_t feat = p.epilogue == kMxSwiglu ? 128 : 256;
-  const int64_t pairs = (int64_t)((p.rows + 127) / 128) * ((p.n_out + feat - 1) / feat);
+  if (tiles(128) * ((p.n_out + feat - 1) / feat) < 2 * kCus)
+    return launch_wide_any<Geo<2, 2, 2, 2, 2, 2>>(p, s);
   const int mean = p.rows / p.E;
-  if (mean <= 64 || pairs < 2 * kCus) return launch_wide_any<Geo<4, 1, 2, 2, 3>>(p, s);
-  if (mean <= 192) return launch_wide_any<Geo<2, 2, 2, 3, 3>>(p, s);
-  return launch_wide_any<Geo<4, 2, 2, 2, 4>>(p, s);
+  if (mean <= 64) return launch_wide_any<Geo<4, 1, 2, 2, 1, 3>>(p, s);
+  if (mean <= 192) return launch_wide_any<Geo<2, 2, 2, 3, 1, 3>>(p, s);
+  return launch_wide_any<Geo<4, 2, 2, 4, 2, 2>>(p, s);
 }
 
 }  // namespace moe

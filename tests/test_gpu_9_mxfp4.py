@@ -150,11 +150,14 @@ SHAPES = [  # T, K, E, N, k, gather, skew
     (130, 4, 16, 256, 512, True, 0.7), (300, 1, 3, 288, 896, False, 1.5), (257, 6, 64, 64, 1024, True, 0.2),
     (64, 8, 2048, 32, 128, True, 0.0), (700, 2, 3, 512, 256, True, 3.0), (1000, 1, 1, 384, 1152, False, 0.0),
     (1600, 4, 16, 320, 384, True, 0.1), (2500, 2, 9, 128, 640, False, 0.4),
-    # the wide kernel's three tiles, with scale bytes in pieces of 16 and of 4, a last stage of 128
-    # values, and columns that end inside a tile
+    # the wide kernel's tiles (two shapes for each: scale bytes in pieces of 16 and of 4), a last stage
+    # of 128 values, columns that end inside a tile
+    (1024, 1, 1, 1024, 1024, True, 0.0), (1300, 1, 3, 1056, 128, False, 0.5),
     (900, 2, 40, 512, 512, True, 0.5), (900, 2, 40, 544, 128, False, 0.5),
-    (2048, 4, 64, 2048, 512, True, 0.3), (2051, 4, 64, 2080, 640, False, 0.3),
-    (2047, 4, 16, 2080, 1024, True, 0.5), (2048, 4, 16, 2048, 384, True, 2.0)]
+    (1200, 4, 200, 1024, 512, True, 0.1), (1200, 4, 200, 1056, 640, False, 0.1),
+    (1200, 4, 200, 1056, 128, True, 1.0), (2048, 4, 64, 2048, 512, True, 0.3),
+    (2051, 4, 64, 2080, 640, False, 0.3), (2047, 4, 16, 2080, 1024, True, 0.5),
+    (2048, 4, 16, 2048, 384, True, 2.0)]
 
 
 @pytest.mark.parametrize("epi", [abi.MX_F32, abi.MX_BF16, abi.MX_SWIGLU_MXFP4])
@@ -215,7 +218,8 @@ def test_mm_scales_at_any_4_byte_address():
 
 
 @pytest.mark.parametrize("T,K,E,N,k", [(50, 3, 6, 64, 256), (3000, 3, 50, 640, 256),
-                                       (3000, 3, 70, 2048, 256), (3000, 3, 30, 2048, 256)])
+                                       (1200, 4, 200, 1024, 256), (3000, 3, 70, 2048, 256),
+                                       (3000, 3, 30, 2048, 256)])
 def test_mm_rows_past_the_experts_are_left_alone(T, K, E, N, k):
     """Routes to ids outside [0, E) take rows past offsets[E]: those keep their bytes, in every epilogue."""
     rng = np.random.default_rng(3)
