@@ -2,10 +2,9 @@
 // token t's E logits, n the valid tokens, c[e] how many of their K routes each went to expert e:
 //   f[e] = c[e] / (n K),   P[e] = (1/n) sum_t p[t, e],   loss = E sum_e f[e] P[e],
 //   d loss / d logits[t, j] = (E / n) p[t, j] (f[j] - sum_e f[e] p[t, e]),
-// the counts being constants of the gradient.  Since sum_e p[t, e] = 1, f may be replaced by its
-// difference from its mean in the bracket, and is: near balance f is almost constant and the bracket
-// a small difference of large terms otherwise.  f[e] - mean = (c[e] E - N) / (E n K), N = sum c:
-// exact integers up to one rounding.
+// the counts being constants of the gradient.  Since sum_e p[t, e] = 1, f may be replaced by f - 1/E
+// in the bracket, and is: near balance f is almost constant and the bracket a small difference of
+// large terms otherwise.  f[e] - 1/E = (c[e] E - n K) / (E n K), exact integers up to one rounding.
 //
 // A row of logits is one wavefront's, read once into registers, the next row's loads under way
 // meanwhile (-inf: an expert that the token may not take; a row of nothing else has p = 0).  Forward:
@@ -275,22 +274,19 @@ __global__ __launch_bounds__(kWaves * 64) void balance_backward_kernel(
   fetch();
   const int n = counts[a.E];
   int32_t c[VPL];
-  int64_t total = 0;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
     c[j] = 0;
     if (column<VEC>(j, lane) < a.E) c[j] = counts[column<VEC>(j, lane)];
-    total += c[j];
   }
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o);
-  // g (E / n) (f - mean) = g (c E - N) / (n n K)
+  // g (E / n) (f - 1/E) = g (c E - n K) / (n n K)
   const float nf = (float)n;
   const float scale =
       n > 0 ? (grad_loss ? *grad_loss : 1.0f) / (nf * (float)a.K) / nf : 0.0f;
   float dev[VPL];
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) dev[j] = (float)((int64_t)c[j] * a.E - total) * scale;
+  for (int j = 0; j < VPL; ++j)
+    dev[j] = (float)((int64_t)c[j] * a.E - (int64_t)n * a.K) * scale;
   while (t < a.T) {
     const R now = row;
     const bool live = on;

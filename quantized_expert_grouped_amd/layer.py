@@ -85,6 +85,94 @@ class MoePrefillLayer:
         return self.ws[off:off + nbytes]
 
 
+class MoeMxfp4Layer:
+    """The layer over experts in MXFP4, held on one GPU: routing, maps, the tokens quantised once, gate/up
+    with SwiGLU and requantisation, down into bf16 rows, combine.  gate_up [E, 2F, H] (gate's F rows,
+    then up's) and down [E, H, F]: floating-point tensors, quantised here once, or (codes, scales)
+    pairs.  H and F: multiples of 128.  A layer's calls share its buffers, so they must not overlap."""
+
+    def __init__(self, gate_up, down, max_tokens: int, K: int, device="cuda"):
+        self.device = torch.device(device)
+        self.gate_up, self.down = self._weights(gate_up), self._weights(down)
+        self.E, f2, hb = self.gate_up[0].shape
+        self.H, self.F = 2 * hb, f2 // 2
+        if self.down[0].shape != (self.E, self.H, self.F // 2) or f2 % 2:
+            raise ValueError("gate_up [E, 2F, H] and down [E, H, F] do not fit each other")
+        if self.H % 128 or self.F % 128 or not 1 <= K <= self.E:
+            raise ValueError("H and F are multiples of 128, K one of 1 .. E")
+        self.max_tokens, self.K = max_tokens, K
+        R = max_tokens * K
+        self.counts, self.offsets = self._i32(self.E), self._i32(self.E + 1)
+        self.src, self.slot = self._i32(R), self._i32(R)
+        self.order, self.n_active = self._i32(self.E), self._i32(1)
+        self.maps_ws = self._u8(abi.build_maps_workspace_size(max_tokens, K, self.E))
+        self.x_codes, self.x_scales = self._u8(max_tokens, self.H // 2), self._u8(max_tokens, self.H // 32)
+        self.h_codes, self.h_scales = self._u8(R, self.F // 2), self._u8(R, self.F // 32)
+        self.rows = torch.empty((R, self.H), dtype=torch.bfloat16, device=self.device)
+        self.balance_ws = self._u8(abi.balance_workspace_size(max_tokens, self.E))
+
+    def _u8(self, *shape):
+        return torch.empty(shape, dtype=torch.uint8, device=self.device)
+
+    def _i32(self, n: int):
+        return torch.empty(n, dtype=torch.int32, device=self.device)
+
+    def _weights(self, w):
+        if isinstance(w, (tuple, list)):
+            return tuple(_to_device(t, torch.uint8, self.device) for t in w)
+        w = w.to(self.device).contiguous()
+        E, N, k = w.shape
+        codes, scales = self._u8(E, N, k // 2), self._u8(E, N, k // 32)
+        abi.mxfp4_quantize(w.view(E * N, k), codes.view(E * N, -1), scales.view(E * N, -1))
+        return codes, scales
+
+    def _tokens(self, t: torch.Tensor) -> int:
+        if t.shape[0] > self.max_tokens:
+            raise ValueError(f"T={t.shape[0]} exceeds the buffers' {self.max_tokens} tokens")
+        return t.shape[0]
+
+    def route(self, logits: torch.Tensor):
+        T = logits.shape[0]
+        idx = torch.empty((T, self.K), dtype=torch.int32, device=self.device)
+        w = torch.empty((T, self.K), dtype=torch.float32, device=self.device)
+        abi.route_topk(logits, self.K, idx, w)
+        return idx, w
+
+    def balance(self, logits: torch.Tensor, idx: torch.Tensor, valid: torch.Tensor | None = None,
+                grad_loss: torch.Tensor | None = None):
+        """The router's counts int32 [E + 1] (the valid tokens last), mean probabilities, balance loss
+        and the loss's gradient (times grad_loss) with respect to the logits."""
+        self._tokens(logits)
+        counts, prob = self._i32(self.E + 1), torch.empty(self.E, device=self.device)
+        loss, grad = torch.empty(1, device=self.device), torch.empty_like(logits)
+        abi.balance_loss(logits, idx, counts, prob, loss, self.balance_ws, valid=valid)
+        abi.balance_loss_backward(logits, counts, self.K, grad, valid=valid, grad_loss=grad_loss)
+        return counts, prob, loss, grad
+
+    def forward(self, x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+        T = self._tokens(x)
+        R = T * self.K
+        if out is None:
+            out = torch.empty((T, self.H), dtype=torch.float32, device=self.device)
+        src, slot, rows = self.src[:R], self.slot[:R], self.rows[:R]
+        x_codes, x_scales = self.x_codes[:T], self.x_scales[:T]
+        h_codes, h_scales = self.h_codes[:R], self.h_scales[:R]
+        abi.build_maps(idx, self.E, 0, self.counts, self.offsets, src, slot, self.order,
+                       self.n_active, self.maps_ws)
+        abi.mxfp4_quantize(x, x_codes, x_scales)
+        abi.mxfp4_mm_grouped(*self.gate_up, self.offsets, x_codes, x_scales, h_codes, src=src,
+                             K=self.K, out_scales=h_scales)
+        abi.mxfp4_mm_grouped(*self.down, self.offsets, h_codes, h_scales, rows)
+        abi.combine_bf16(rows, slot, w, out)
+        return out
+
+    def step(self, x: torch.Tensor, logits: torch.Tensor, out: torch.Tensor | None = None):
+        """One pass of the whole path: routing, then the layer."""
+        idx, w = self.route(logits)
+        return self.forward(x, idx, w, out)
+
+
 def _to_device(a, dtype, device):
     if isinstance(a, torch.Tensor):
         return a.to(device=device, dtype=dtype).contiguous()

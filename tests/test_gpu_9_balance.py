@@ -69,8 +69,8 @@ def check(xt, idx, v, dtype, g, got):
     assert np.all(np.abs(host(got[1]) - prob) <= dprob)
     dl = E * float(f @ dprob) + loss * (E / 256 + 24) * 2.0 ** -24
     assert abs(float(host(got[2])[0]) - loss) <= dl + 2.0 ** -126
-    # gradient: p (f_j - N - sum p (f - N)) with the mean N taken out; f - N to 8 roundings
-    dev_f = f - f.sum() / E
+    # gradient: p (f_j - 1/E - sum p (f - 1/E)); f - 1/E to 8 roundings
+    dev_f = f - 1.0 / E
     dot_abs = (p * np.abs(dev_f)).sum(1, keepdims=True)
     err = p * (np.abs(dev_f) + dot_abs) * (eps + (p * eps).sum(1, keepdims=True) + (E / 64 + 24) * 2.0 ** -24)
     err = err + tiny * (np.abs(dev_f) + dot_abs)

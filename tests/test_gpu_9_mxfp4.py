@@ -7,6 +7,7 @@ import torch
 import mxref
 from gpu_util import dev, empty, gpu_maps, host, note
 from quantized_expert_grouped_amd import abi
+from quantized_expert_grouped_amd.layer import MoeMxfp4Layer
 
 pytestmark = pytest.mark.gpu
 
@@ -443,3 +444,27 @@ def test_path_replays_from_a_graph_and_on_two_streams():
                 p.run()
     for p, wt in zip(ps, want):
         assert all(np.array_equal(a, b) for a, b in zip(p.bytes(), wt))
+
+
+def test_layer_is_the_path():
+    """MoeMxfp4Layer's results are the path's bytes, for fewer tokens than its buffers hold, after a call of
+    another size, from (codes, scales) and from float weights that those stand for."""
+    p = Path(45, 256, 128, 16, 2, 9)
+    p.run()
+    want = p.bytes()[-1]
+    floats = [torch.empty((m[0].shape[0], m[0].shape[1], 2 * m[0].shape[2]), device="cuda") for m in (p.gu, p.dn)]
+    for f, m in zip(floats, (p.gu, p.dn)):
+        abi.mxfp4_dequantize(m[0].flatten(0, 1), m[1].flatten(0, 1), f.flatten(0, 1))
+    for gate_up, down in ((p.gu, p.dn), floats):
+        layer = MoeMxfp4Layer(gate_up, down, max_tokens=70, K=2)
+        assert (layer.E, layer.H, layer.F) == (16, 256, 128)
+        layer.step(torch.randn(70, 256, device="cuda"), torch.randn(70, 16, device="cuda"))
+        out = layer.step(p.x, p.logits)
+        assert np.array_equal(host(out).view(np.uint8), want)
+        idx, _ = layer.route(p.logits)
+        for got, ref in zip(layer.balance(p.logits, idx), (p.counts, p.prob, p.loss, p.grad)):
+            assert torch.equal(got, ref)
+        with pytest.raises(ValueError):
+            layer.step(torch.randn(71, 256, device="cuda"), torch.randn(71, 16, device="cuda"))
+    with pytest.raises(ValueError):
+        MoeMxfp4Layer(p.gu, p.gu, max_tokens=4, K=2)
