@@ -426,8 +426,9 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
 int moe_mxfp4_quantize(const void *x, int dtype, int64_t ldx, int rows, int n, void *codes,
                        void *scales, void *stream);
 
-/* The values that codes and scales stand for, exactly: y [rows x n] in MOE_F32 or MOE_BF16 (MOE_F16,
- * whose range is smaller, is refused), rows ldy values apart.  Alignment as above. */
+/* The values that codes and scales stand for: y [rows x n] in MOE_F32 or MOE_BF16 (MOE_F16, whose
+ * range is smaller, is refused), rows ldy values apart.  Exact, but for 4 and 6 times 2^127, which
+ * are infinite.  Alignment as above. */
 int moe_mxfp4_dequantize(const void *codes, const void *scales, int rows, int n, void *y,
                          int dtype, int64_t ldy, void *stream);
 

@@ -2,15 +2,16 @@
 // token t's E logits, n the valid tokens, c[e] how many of their K routes each went to expert e:
 //   f[e] = c[e] / (n K),   P[e] = (1/n) sum_t p[t, e],   loss = E sum_e f[e] P[e],
 //   d loss / d logits[t, j] = (E / n) p[t, j] (f[j] - sum_e f[e] p[t, e]),
-// the counts being constants of the gradient.  Since sum_e p[t, e] = 1, f may be replaced by f - 1/E
-// in the bracket, and is: near balance f is almost constant and the bracket a small difference of
-// large terms otherwise.  f[e] - 1/E = (c[e] E - n K) / (E n K), exact integers up to one rounding.
+// the counts being constants of the gradient.  Since sum_e p[t, e] = 1, f may be replaced by f -
+// 1/E in the bracket, and is: near balance f is almost constant and the bracket a small difference
+// of large terms otherwise.  f[e] - 1/E = (c[e] E - n K) / (E n K), exact integers up to one
+// rounding.
 //
 // A row of logits is one wavefront's, read once into registers, the next row's loads under way
-// meanwhile (-inf: an expert that the token may not take; a row of nothing else has p = 0).  Forward:
-// each workgroup keeps its rows' sums of p per column in registers and its counts in LDS and leaves
-// one row of partial sums; a second launch adds those, and its last workgroup (an integer ticket)
-// forms the loss.  All float sums are in an order that depends on the sizes alone.
+// meanwhile (-inf: an expert that the token may not take; a row of nothing else has p = 0).
+// Forward: each workgroup keeps its rows' sums of p per column in registers and its counts in LDS
+// and leaves one row of partial sums; a second launch adds those, and its last workgroup (an
+// integer ticket) forms the loss.  All float sums are in an order that depends on the sizes alone.
 #include <math.h>
 
 #include <type_traits>
@@ -46,8 +47,8 @@ __device__ __forceinline__ Partials partials(void* ws, int groups, int E) {
   return q;
 }
 
-// The wavefront's largest value, or sum: DPP steps leave each row of 16 lanes with its row's, then the
-// four rows' are read into scalars.
+// The wavefront's largest value, or sum: DPP steps leave each row of 16 lanes with its row's, then
+// the four rows' are read into scalars.
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
@@ -190,7 +191,8 @@ __global__ __launch_bounds__(kWaves * 64) void balance_rows_kernel(BalanceArgs a
   if (threadIdx.x == 0) q.tokens[blockIdx.x] = tokens;
 }
 
-// 32 columns by 32 strands of workgroups' partial rows, 8 of them each, all loads under way at once.
+// 32 columns by 32 strands of workgroups' partial rows, 8 of them each, all loads under way at
+// once.
 __global__ __launch_bounds__(1024) void balance_join_kernel(int E, int K, int groups, void* ws,
                                                             int32_t* __restrict__ counts,
                                                             float* __restrict__ prob_mean,

@@ -45,8 +45,9 @@ __device__ __forceinline__ float mx_amax(float m, float v) {
 }
 
 // The 8 codes (value i in nibble i) of 8 values of a block with this scale byte.
-// v_cvt_scalef32_pk_fp4_f32 divides by the power of two that its scale operand's exponent field stands for
-// (0: 2^-127), rounds to the nearest, ties to even, and gives 6 beyond 6; tested for every border and scale.
+// v_cvt_scalef32_pk_fp4_f32 divides by the power of two that its scale operand's exponent field
+// stands for (0: 2^-127), rounds to the nearest, ties to even, and gives 6 beyond 6; tested for
+// every border and scale.
 __device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], uint32_t byte) {
   const float scale = __uint_as_float(byte << 23);
   uint32_t w = 0;

@@ -2,8 +2,8 @@
 // least-routed experts to the idle CPU pool", "What it does": Dm's rows are unweighted, the combine
 // applies the routing weights):
 //   out[t, i] = sum_{k < K} w[t, k] * rows[slot[t*K + k], i],
-// k ascending, fp32 fused multiply-adds, each bf16 value widened exactly.  A route whose slot is no row (-1:
-// its expert id was out of range) adds nothing.
+// k ascending, fp32 fused multiply-adds, each bf16 value widened exactly.  A route whose slot is no
+// row (-1: its expert id was out of range) adds nothing.
 #include "mx.hpp"
 
 namespace moe {
@@ -13,9 +13,9 @@ namespace {
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-// A thread owns 8 columns of a token and keeps up to kBatch rows' loads under way (each row is read once:
-// non-temporal); the token's slots and weights are scalars.  Bound by memory: 8192 tokens, K = 10,
-// H = 2048 (403 MB).
+// A thread owns 8 columns of a token and keeps up to kBatch rows' loads under way (each row is read
+// once: non-temporal); the token's slots and weights are scalars.  Bound by memory: 8192 tokens, K
+// = 10, H = 2048 (403 MB).
 constexpr int kBatch = 8;
 
 __global__ __launch_bounds__(256) void combine_bf16_kernel(const uint16_t* __restrict__ rows,

@@ -3,12 +3,12 @@
 // which v_mfma_scale_f32_32x32x64_f8f6f4 computes whole: e2m1 codes and the blocks' scale bytes go
 // in as they lie in memory, sums stay in fp32.
 //
-// Operands: the weights are the MFMA's A (its rows are output columns n), the activations its B (its
-// columns are routed rows), so a lane's 16 results are 4 runs of 4 consecutive n of one routed
-// row.  Lane l of an operand holds one block of one row: row l % 32 and, of the MFMA's two blocks, l / 32,
-// as 16 bytes of codes and one scale byte (a byte of a register that the instruction picks).  The order
-// in which blocks are taken is free as long as both operands agree, so a lane takes runs of
-// consecutive blocks.
+// Operands: the weights are the MFMA's A (its rows are output columns n), the activations its B
+// (its columns are routed rows), so a lane's 16 results are 4 runs of 4 consecutive n of one routed
+// row.  Lane l of an operand holds one block of one row: row l % 32 and, of the MFMA's two blocks,
+// l / 32, as 16 bytes of codes and one scale byte (a byte of a register that the instruction
+// picks).  The order in which blocks are taken is free as long as both operands agree, so a lane
+// takes runs of consecutive blocks.
 #include <algorithm>
 #include <type_traits>
 
@@ -32,13 +32,13 @@ __device__ __forceinline__ v16f mfma_mx(const v4i& w, const v4i& a, const v16f& 
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, a8, c, kFp4, kFp4, SEL, sw, SEL, sa);
 }
 
-// The expert whose tile `id` is, and the tile's rows.  Tiles of BM = 32 rows are numbered without a pass
-// over the experts' counts: expert e's start at offsets[e] / BM + e, which leaves room for all of
-// them (ceil(n / BM) <= (offsets[e] + n) / BM - offsets[e] / BM + 1) and grows by one at least
+// The expert whose tile `id` is, and the tile's rows.  Tiles of BM = 32 rows are numbered without a
+// pass over the experts' counts: expert e's start at offsets[e] / BM + e, which leaves room for all
+// of them (ceil(n / BM) <= (offsets[e] + n) / BM - offsets[e] / BM + 1) and grows by one at least
 // from expert to expert, so a tile's expert is the last one whose first number is not above it.
-// Some numbers belong to no tile: those workgroups end.  With fewer rows than that gives numbers, a tile is
-// numbered by its first row instead (`by_row`).  The lanes compare 64 experts at a time, up to 512
-// experts' loads in flight together.
+// Some numbers belong to no tile: those workgroups end.  With fewer rows than that gives numbers, a
+// tile is numbered by its first row instead (`by_row`).  The lanes compare 64 experts at a time, up
+// to 512 experts' loads in flight together.
 struct Tile {
   int expert, row0, nrows;
 };
@@ -70,25 +70,25 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, i
   return t;
 }
 
-// silu(g) * u in fp32 with the hardware's exponential and reciprocal, 1 ulp each; the rounding of the
-// exponent's argument adds |g| 2^-24.  g far below zero gives g * (1 / inf) = -0.
+// silu(g) * u in fp32 with the hardware's exponential and reciprocal, 1 ulp each; the rounding of
+// the exponent's argument adds |g| 2^-24.  g far below zero gives g * (1 / inf) = -0.
 __device__ __forceinline__ float swiglu(float g, float u) {
   const float e = __builtin_amdgcn_exp2f(g * -1.44269504088896341f);
   return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
-// ---- few rows ------------------------------------------------------------------------------
-// One workgroup: up to 32 rows of an expert by 32 columns (SwiGLU: 32 gates and their 32 ups), K
-// split over its 4 wavefronts and joined in LDS.  With so few rows a call is bound by latency: each wavefront
-// loads its operands from memory straight into the MFMA's layout, with no stage or barrier before the
-// join.  One token's ten rows, gate/up (11 MB of weights): 7.0 us; down: 4.6 us.
+// ---- few rows ------------------------------------------------------------------------------ One
+// workgroup: up to 32 rows of an expert by 32 columns (SwiGLU: 32 gates and their 32 ups), K split
+// over its 4 wavefronts and joined in LDS.  With so few rows a call is bound by latency: each
+// wavefront loads its operands from memory straight into the MFMA's layout, with no stage or
+// barrier before the join.  One token's ten rows, gate/up (11 MB of weights): 7.0 us; down: 4.6 us.
 template <int EPI>
 __global__ __launch_bounds__(256) void mx_mm_narrow_kernel(MxProblem p, bool by_row) {
   constexpr int kMats = EPI == kMxSwiglu ? 2 : 1;
   __shared__ float part[4][kMats][32][36];
   const Tile t = find_tile(p.offsets, p.E, p.rows, blockIdx.x, by_row);
   if (t.nrows <= 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31;
   const int n0 = blockIdx.y * 32;
   const size_t kb = p.k_in / 2, sb = p.k_in / kMxBlock;
@@ -108,18 +108,36 @@ __global__ __launch_bounds__(256) void mx_mm_narrow_kernel(MxProblem p, bool by_
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[m][i] = 0.0f;
 
-  for (int c = wave; c < p.k_in / 128; c += 4) {
-    const v4i a0 = *reinterpret_cast<const v4i*>(a + c * 64);
-    const v4i a1 = *reinterpret_cast<const v4i*>(a + c * 64 + 16);
-    const int sa = *reinterpret_cast<const uint16_t*>(as + c * 4);
+  // 128 values at a time, up to kBatch times' loads under way before the first products
+  constexpr int kBatch = 4;
+  const int chunks = p.k_in / 128;
+  for (int c0 = wave; c0 < chunks; c0 += 4 * kBatch) {
+    v4i av[kBatch][2], wv[kBatch][kMats][2];
+    int sa[kBatch], sw[kBatch][kMats];
 #pragma unroll
-    for (int m = 0; m < kMats; ++m) {
-      const uint8_t* wm = w + m * up * kb + c * 64;
-      const v4i w0 = *reinterpret_cast<const v4i*>(wm);
-      const v4i w1 = *reinterpret_cast<const v4i*>(wm + 16);
-      const int sw = *reinterpret_cast<const uint16_t*>(ws + m * up * sb + c * 4);
-      acc[m] = mfma_mx<0>(w0, a0, acc[m], sw, sa);
-      acc[m] = mfma_mx<1>(w1, a1, acc[m], sw, sa);
+    for (int b = 0; b < kBatch; ++b) {
+      const int c = c0 + 4 * b;
+      if (c >= chunks) break;  // uniform
+      const v4i* ap = reinterpret_cast<const v4i*>(a + c * 64);
+      av[b][0] = ap[0];
+      av[b][1] = ap[1];
+      sa[b] = *reinterpret_cast<const uint16_t*>(as + c * 4);
+#pragma unroll
+      for (int m = 0; m < kMats; ++m) {
+        const v4i* wp = reinterpret_cast<const v4i*>(w + m * up * kb + c * 64);
+        wv[b][m][0] = wp[0];
+        wv[b][m][1] = wp[1];
+        sw[b][m] = *reinterpret_cast<const uint16_t*>(ws + m * up * sb + c * 4);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (c0 + 4 * b >= chunks) break;
+#pragma unroll
+      for (int m = 0; m < kMats; ++m) {
+        acc[m] = mfma_mx<0>(wv[b][m][0], av[b][0], acc[m], sw[b][m], sa[b]);
+        acc[m] = mfma_mx<1>(wv[b][m][1], av[b][1], acc[m], sw[b][m], sa[b]);
+      }
     }
   }
 #pragma unroll
@@ -176,12 +194,12 @@ typedef __attribute__((address_space(3))) const void* lds_ptr_t;
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(lds_ptr_t)p;
 }
-// Direct global->LDS loads: lane i's 16 (4) bytes land at lds + 16 i (4 i), lds wave-uniform (M0); a
-// lane's source is a uniform base and an offset of its own.  As inline assembly, so that the compiler does
-// not wait for them at every LDS read (it cannot tell the buffers apart): the kernel waits for them itself.
-// Nor does it then keep the distance between a vector instruction that writes a scalar register (a
-// readlane, as it restores spilled scalars) and a load that takes its address from it, 5 wait states: the
-// s_nop does, and covers the one that M0 needs.
+// Direct global->LDS loads: lane i's 16 (4) bytes land at lds + 16 i (4 i), lds wave-uniform (M0);
+// a lane's source is a uniform base and an offset of its own.  As inline assembly, so that the
+// compiler does not wait for them at every LDS read (it cannot tell the buffers apart): the kernel
+// waits for them itself. Nor does it then keep the distance between a vector instruction that
+// writes a scalar register (a readlane, as it restores spilled scalars) and a load that takes its
+// address from it, 5 wait states: the s_nop does, and covers the one that M0 needs.
 __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
   asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" : : "{m0}"(lds), "v"(off), "s"(base) : "memory");
 }
@@ -189,10 +207,10 @@ __device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t
   asm volatile("s_nop 4\n\tglobal_load_lds_dword %1, %2" : : "{m0}"(lds), "v"(off), "s"(base) : "memory");
 }
 
-// A workgroup's tile: BN weight rows by BM routed rows, its wavefronts in WN slices of the columns by WM of
-// the rows, each wavefront TN x TM MFMA tiles; row tiles are dealt to the WM in turn, so that few
-// rows still keep all busy.  A stage is 256 values of K, 128 bytes of each row, in one of NBUF
-// buffers.
+// A workgroup's tile: BN weight rows by BM routed rows, its wavefronts in WN slices of the columns
+// by WM of the rows, each wavefront TN x TM MFMA tiles; row tiles are dealt to the WM in turn, so
+// that few rows still keep all busy.  A stage is 256 values of K, 128 bytes of each row, in one of
+// NBUF buffers.
 constexpr int kStage = 128;
 template <int WN_, int WM_, int TN_, int TM_, int NBUF_, int MINW_>
 struct Geo {
@@ -200,9 +218,10 @@ struct Geo {
   static constexpr int kMinWaves = MINW_;  // wavefronts to fit on a SIMD
   static constexpr int kWaves = WN * WM;
   static constexpr int BN = WN * TN * 32, BM = WM * TM * 32, kRows = BN + BM;
-  // loads of 16 bytes a lane: a stage's weight and routed rows (8 rows each), the scale bytes of 512 values
-  // (64 rows each); or scale bytes of a stage, 4 bytes a lane (32 rows each).  A wavefront issues every
-  // kWaves-th; where they do not come out even, the last is issued more than once.
+  // loads of 16 bytes a lane: a stage's weight and routed rows (8 rows each), the scale bytes of
+  // 512 values (64 rows each); or scale bytes of a stage, 4 bytes a lane (32 rows each).  A
+  // wavefront issues every kWaves-th; where they do not come out even, the last is issued more than
+  // once.
   static constexpr int kW = BN / 8, kA = BM / 8, kS = kRows / 64, kS4 = kRows / 32;
   static constexpr int kWI = (kW + kWaves - 1) / kWaves, kAI = (kA + kWaves - 1) / kWaves;
   static constexpr int kSI = (kS + kWaves - 1) / kWaves, kS4I = (kS4 + kWaves - 1) / kWaves;
@@ -220,17 +239,17 @@ struct Lds {
 // rows then read one piece index from different banks, in groups of 8 as of 16 lanes.
 __device__ __forceinline__ int swizzle(int row) { return ((row >> 1) & 3) | (((row ^ (row >> 3)) & 1) << 2); }
 
-// Waits for the wavefront's loads to LDS, and for its LDS reads: what it read may be overwritten after
-// the barrier.
+// Waits for the wavefront's loads to LDS, and for its LDS reads: what it read may be overwritten
+// after the barrier.
 __device__ __forceinline__ void wait_and_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" : : : "memory");
 }
 
-// A wavefront's loads: uniform bases and its lanes' offsets.  WIDE: scale bytes come
-// 16 of a row at a time (512 values), which K and the scales' alignment have to allow; otherwise 4 at a
-// time, in every stage.
+// A wavefront's loads: uniform bases and its lanes' offsets.  WIDE: scale bytes come 16 of a row at
+// a time (512 values), which K and the scales' alignment have to allow; otherwise 4 at a time, in
+// every stage.
 template <class G, bool WIDE>
 struct Dma {
   static constexpr int kScales = WIDE ? G::kSI : G::kS4I;
@@ -260,8 +279,8 @@ __device__ __forceinline__ void plan_weights(Dma<G, WIDE>& d, int k_in, WR wrow,
     if (row < G::BN) d.so[i] = wrow(row) * sb + d.s_byte(lane);
   }
 }
-// The routed rows' offsets, from the activation rows that arow(i) names.  FIRST: only the loads that arow makes, their
-// results left in ao and so; otherwise the offsets from those.
+// The routed rows' offsets, from the activation rows that arow(i) names.  FIRST: only the loads
+// that arow makes, their results left in ao and so; otherwise the offsets from those.
 template <class G, bool WIDE, bool FIRST, class AR>
 __device__ __forceinline__ void plan_rows(Dma<G, WIDE>& d, int k_in, AR arow, int wave, int lane) {
   const uint32_t kb = k_in / 2, sb = k_in / kMxBlock;
@@ -278,8 +297,8 @@ __device__ __forceinline__ void plan_rows(Dma<G, WIDE>& d, int k_in, AR arow, in
 }
 
 // Load i of a stage's rows to LDS at `rows`, weight rows first; a stage's scale bytes to `scales`.
-// `last_half`: of a last stage of 128 values, whose pieces 4..7 (scale bytes 4..7) do not exist; those
-// lanes load the first ones again, and the products leave them out.
+// `last_half`: of a last stage of 128 values, whose pieces 4..7 (scale bytes 4..7) do not exist;
+// those lanes load the first ones again, and the products leave them out.
 template <class G, bool WIDE>
 __device__ __forceinline__ void issue_row(const Dma<G, WIDE>& d, int i, int stage, uint32_t rows, bool last_half,
                                           int wave, int lane) {
@@ -330,10 +349,11 @@ __device__ __forceinline__ Reads plan_reads(const Lds<G>& lds, int wn, int wm, i
   return r;
 }
 
-// The wavefront's products of one stage, with NL of its TM row tiles holding rows.  rows_at: the stage's
-// buffer; scales_at: its set of scale bytes and place among its row's.  A wavefront that issues a load to LDS
-// waits until the CU has taken it, about 200 clocks while all issue (a fifth to a half of a stage's
-// time if it issues them in a row), so load(i), i < LOADS, are spread over the products, which go on meanwhile.
+// The wavefront's products of one stage, with NL of its TM row tiles holding rows.  rows_at: the
+// stage's buffer; scales_at: its set of scale bytes and place among its row's.  A wavefront that
+// issues a load to LDS waits until the CU has taken it, about 200 clocks while all issue (a fifth
+// to a half of a stage's time if it issues them in a row), so load(i), i < LOADS, are spread over
+// the products, which go on meanwhile.
 template <class G, bool WIDE, int NL, int LOADS, class F>
 __device__ __forceinline__ void products(const Reads& r, int rows_at, int scales_at, v16f (&acc)[G::TN][G::TM],
                                          bool last_half, int lane, F load) {
@@ -398,15 +418,15 @@ __device__ __forceinline__ void products(const Reads& r, int rows_at, int scales
   step(std::integral_constant<int, 3>{});
 }
 
-// A copy that the compiler takes for a new value: what is computed from it stays where it is written instead
-// of being kept in registers through the loops around it.
+// A copy that the compiler takes for a new value: what is computed from it stays where it is
+// written instead of being kept in registers through the loops around it.
 __device__ __forceinline__ int here(int v) {
   asm volatile("" : "+v"(v));
   return v;
 }
 
-// The wavefront's results for one row tile (32 rows from row0, `live` of them real) to memory.  fp32 and bf16 tiles are
-// turned in 4 KiB of LDS, so that 8 lanes write 128 bytes of a row.
+// The wavefront's results for one row tile (32 rows from row0, `live` of them real) to memory.
+// fp32 and bf16 tiles are turned in 4 KiB of LDS, so that 8 lanes write 128 bytes of a row.
 template <class G, int EPI>
 __device__ __forceinline__ void store_tile(const MxProblem& p, const v16f (&acc)[G::TN][G::TM], int i, size_t row0,
                                            int live, int n0, uint8_t* turn, int lane) {
@@ -468,7 +488,8 @@ __device__ __forceinline__ void store_tile(const MxProblem& p, const v16f (&acc)
   }
 }
 
-// Where the workgroup is in its buffers: the one at work, and the sets of scale bytes at work and last loaded.
+// Where the workgroup is in its buffers: the one at work, and the sets of scale bytes at work and
+// last loaded.
 struct Ring {
   int buf = 0, set = -1, loaded = -1;
 };
@@ -481,9 +502,10 @@ __device__ __forceinline__ void issue_stage_scales(const Dma<G, WIDE>& d, int k,
   issue_scales(d, k, lscales + ring.loaded * G::kRows * 16, last_half, wave, lane);
 }
 
-// The tile's products along K.  `between` is called once a stage.  With two buffers each stage's loads are issued
-// among the products of the one before it: its first stage's were before this, and its last stage
-// issues the first of the next tile, which `turn_over` puts in place of this one in d.
+// The tile's products along K.  `between` is called once a stage.  With two buffers each stage's
+// loads are issued among the products of the one before it: its first stage's were before this, and
+// its last stage issues the first of the next tile, which `turn_over` puts in place of this one in
+// d.
 template <class G, bool WIDE, int NL, class F, class A>
 __device__ __forceinline__ void main_loop(const Reads& r, Dma<G, WIDE>& d, Ring& ring, uint32_t lrows,
                                           uint32_t lscales, v16f (&acc)[G::TN][G::TM], int k_in, F between, A turn_over,
@@ -503,7 +525,8 @@ __device__ __forceinline__ void main_loop(const Reads& r, Dma<G, WIDE>& d, Ring&
     if (!WIDE || (k & 1) == 0) ring.set = (ring.set + 1) & (G::NBUF - 1);
     const int scales_at = ring.set * G::kRows * 16 + (WIDE ? (k & 1) * 8 : 0);
     if constexpr (G::NBUF == 2) {
-      // after the products while other wavefronts' still go on; the largest tile has no registers for that
+      // after the products while other wavefronts' still go on; the largest tile has no registers
+      // for that
       constexpr bool kAfter = G::TM <= 2;
       if (!kAfter) between();
       const int kn = k + 1 < stages ? k + 1 : 0;
@@ -531,10 +554,10 @@ __device__ __forceinline__ int scan(int v) {
   return v;
 }
 
-// Workgroups that stay: kPerCu of them on each CU, each with a share of the (row tile, column tile) pairs of all
-// experts, and the next pair's place found and its rows' offsets computed while the products of the one at work
-// go on.  (With a workgroup to a pair those two took 5.8 of its 20.6 us at 8192 tokens, 512 experts,
-// gate/up.)
+// Workgroups that stay: kPerCu of them on each CU, each with a share of the (row tile, column tile)
+// pairs of all experts, and the next pair's place found and its rows' offsets computed while the
+// products of the one at work go on.  (With a workgroup to a pair those two took 5.8 of its 20.6 us
+// at 8192 tokens, 512 experts, gate/up.)
 template <class G, int EPI, bool WIDE>
 __global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kernel(MxProblem p, uint32_t n_tiles) {
   __shared__ Lds<G> lds;
@@ -556,9 +579,9 @@ __global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kerne
   const uint32_t pairs = (uint32_t)__builtin_amdgcn_readlane(upto, 63) * n_tiles;
   before = upto - before;
 
-  // Workgroups go to the 8 XCDs in turn.  Each XCD takes an eighth of the pairs, column tiles fastest, and its
-  // workgroups walk through it side by side: at any time they share a few experts' weights and rows in
-  // the XCD's L2.
+  // Workgroups go to the 8 XCDs in turn.  Each XCD takes an eighth of the pairs, column tiles
+  // fastest, and its workgroups walk through it side by side: at any time they share a few experts'
+  // weights and rows in the XCD's L2.
   const uint32_t xcd = blockIdx.x & 7, step = gridDim.x >> 3;
   const uint32_t end = (uint32_t)((uint64_t)pairs * (xcd + 1) >> 3);
   uint32_t pair = (uint32_t)((uint64_t)pairs * xcd >> 3) + (blockIdx.x >> 3);
@@ -571,8 +594,8 @@ __global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kerne
   Tile t, u;
   int n0, un0, piece = 0;
   int at = 0;  // how far the next pair is
-  // The next pair in three steps, each of which uses what the one before has loaded: its segment of the
-  // offsets; its tile, and the activation rows; all offsets.
+  // The next pair in three steps, each of which uses what the one before has loaded: its segment of
+  // the offsets; its tile, and the activation rows; all offsets.
   auto advance = [&](uint32_t next) {
     if (at == 0) {
       const int q = (int)(next / n_tiles);
@@ -723,8 +746,8 @@ hipError_t launch_wide_any(const MxProblem& p, hipStream_t s) {
 
 }  // namespace
 
-// Which kernel, by sizes alone (us, MI355X; columns: the narrow kernel, then the wide one's tiles, whose
-// last two have two buffers):
+// Which kernel, by sizes alone (us, MI355X; columns: the narrow kernel, then the wide one's tiles,
+// whose last two have two buffers):
 //                                   narrow  256 x 64  128 x 192  256 x 256  128 x 128
 //   gate/up 2048 -> 2 x 512, 512 experts, K = 10
 //     1 token                          7.0      11.8                              9.3
@@ -745,7 +768,8 @@ hipError_t launch_wide_any(const MxProblem& p, hipStream_t s) {
 // tiles would not fill the CUs twice; then the tile's height goes by the rows an expert has.
 hipError_t launch_mx_mm(const MxProblem& p_, hipStream_t s) {
   MxProblem p = p_;
-  // n / K = n * k_mul >> k_shift for n < 2^30, K <= 64: k_mul K - 2^k_shift <= K <= 2^(k_shift - 30)
+  // n / K = n * k_mul >> k_shift for n < 2^30, K <= 64: k_mul K - 2^k_shift <= K <= 2^(k_shift -
+  // 30)
   p.k_shift = 30;
   while (1 << (p.k_shift - 30) < p.K) ++p.k_shift;
   p.k_mul = (uint32_t)(((uint64_t)1 << p.k_shift) / p.K + 1);

@@ -53,9 +53,10 @@ def check(xt, idx, v, dtype, g, got):
     counts, prob, loss, grad, p, f = mxref.balance(x, idx, v)
     n = max(int(counts[E]), 1)
     assert np.array_equal(host(got[0]), counts)
-    # a probability: 2^t within 2 ulp, t = d log2 e of a rounded difference d by a rounded constant (each a
-    # relative 2^-24 of t at most, the constant's a quarter of that: 2.25 |d| 2^-24 of the power), the
-    # sum of E terms over a lane's E / 64 and 6 steps across lanes, the quotient, the product
+    # a probability: 2^t within 2 ulp, t = d log2 e of a rounded difference d by a rounded constant
+    # (each a relative 2^-24 of t at most, the constant's a quarter of that: 2.25 |d| 2^-24 of the
+    # power), the sum of E terms over a lane's E / 64 and 6 steps across lanes, the quotient, the
+    # product
     on = np.ones(T, bool) if v is None else v != 0
     fin = np.isfinite(x) & on[:, None]
     d = np.where(fin, np.where(fin, x, -1e300).max(1, keepdims=True) - np.where(fin, x, 0.0), 0.0)
@@ -63,7 +64,8 @@ def check(xt, idx, v, dtype, g, got):
     eps = eps + (p * eps).sum(1, keepdims=True)      # the sum's own terms carry theirs
     tiny = 2.0 ** -126                               # smaller exponentials may be flushed
     dp = p * eps + tiny
-    # a column's sum: at most T / groups / 16 + 16 + 256 / 8 + 8 additions of positive terms, and 1 / n
+    # a column's sum: at most T / groups / 16 + 16 + 256 / 8 + 8 additions of positive terms, and 1
+    # / n
     adds = T / min(T, 256) / 16 + 60
     dprob = dp.sum(0) / n + prob * adds * 2.0 ** -24
     assert np.all(np.abs(host(got[1]) - prob) <= dprob)
@@ -144,7 +146,8 @@ def test_gradient_against_differences_of_the_loss():
             d = np.zeros((T, E))
             d[t, j] = step
             diff = (mxref.balance(x + d, idx, v)[2] - mxref.balance(x - d, idx, v)[2]) / (2 * step)
-            # a third derivative of p is at most p, times f E / n: 8 * step^2 bounds it, besides fp32
+            # a third derivative of p is at most p, times f E / n: 8 * step^2 bounds it, besides
+            # fp32
             assert abs(diff - gr[t, j]) <= 8 * step ** 2 + 1e-6
 
 
