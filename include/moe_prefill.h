@@ -445,14 +445,14 @@ typedef enum {
  *   y[r, n] = sum_k A[a(r), k] * W[e, n, k],   a(r) = src ? src[r] / K : r,
  * products and sums in fp32.  w_codes, w_scales: E matrices of n_out rows of k_in values (2 n_out
  * rows for MOE_MX_SWIGLU_MXFP4: gate, then up).  a_codes, a_scales: n_act rows of k_in values;
- * src (int32 [rows], moe_build_maps' src with its K) may be NULL, and K is then not looked at: row r reads
- * activation row r and n_act >= rows.  rows: the rows that out holds; rows from offsets[E] on
- * are left as they were.  An a(r) outside [0, n_act) is a caller error that stays in bounds:
+ * src (int32 [rows], moe_build_maps' src with its K) may be NULL, and K is then not looked at: row
+ * r reads activation row r and n_act >= rows.  rows: the rows that out holds; rows from offsets[E]
+ * on are left as they were.  An a(r) outside [0, n_act) is a caller error that stays in bounds:
  * the row nearest is read.  The order of the fp32 sums depends on the sizes alone.
- * codes and out 16-byte aligned, scales 4-byte (else MOE_EINVAL; 16-byte aligned scales are faster where
- * k_in is a multiple of 512).  MOE_EUNSUPPORTED: n_out not a multiple of 32 or above 2^21, k_in not one of 128,
- * E > MOE_MAX_E, K > MOE_MAX_K, an expert's codes or a_codes of 4 GiB or more, rows above 2^28 - 32 E,
- * (rows / 32 + E) (n_out / 32) of 2^31 or more. */
+ * codes and out 16-byte aligned, scales 4-byte (else MOE_EINVAL; 16-byte aligned scales are faster
+ * where k_in is a multiple of 512).  MOE_EUNSUPPORTED: n_out not a multiple of 32 or above 2^21,
+ * k_in not one of 128, E > MOE_MAX_E, K > MOE_MAX_K, an expert's codes or a_codes of 4 GiB or more,
+ * rows above 2^28 - 32 E, (rows / 32 + E) (n_out / 32) of 2^31 or more. */
 int moe_mxfp4_mm_grouped(const void *w_codes, const void *w_scales, int n_out, int k_in,
                          const int32_t *offsets, int E, const void *a_codes, const void *a_scales,
                          int n_act, const int32_t *src, int K, int rows, int epilogue, void *out,
@@ -472,10 +472,11 @@ int moe_combine_bf16(const void *rows, const int32_t *slot, const float *topk_w,
  *   f[e] = c[e] / (n K),   prob_mean[e] = (1/n) sum_t p[t, e],   loss = E sum_e f[e] prob_mean[e],
  * 1 when both are uniform.  counts int32 [E + 1]: c, then n.  With n = 0 all are 0.
  * A logit of -inf is an expert the token may not take; a valid token with nothing else has p = 0 and
- * counts in n.  NaN and +inf in a valid row: unspecified (in an invalid one they are not looked
- * at).  Sums are in fp32 and in an order that depends on the sizes alone: the same call gives
- * the same bits.  logits: `dtype` values [T x E], rows ld values apart (ld >= E).
- * ws: moe_balance_workspace_size(T, E) bytes, 4-byte aligned.  E <= MOE_MAX_E, K <= min(E, MOE_MAX_K). */
+ * counts in n.  NaN or +inf in a valid row makes p[t] NaN, and with it prob_mean, the loss and the
+ * row's gradient (an invalid row is not looked at).  Sums are in fp32 and in an order that depends
+ * on the sizes alone: the same call gives the same bits.  logits: `dtype` values [T x E], rows ld values apart (ld >= E).
+ * ws: moe_balance_workspace_size(T, E) bytes, 4-byte aligned.  E <= MOE_MAX_E,
+ * K <= min(E, MOE_MAX_K). */
 size_t moe_balance_workspace_size(int T, int E);   /* 0 for sizes the call would refuse */
 int moe_balance_loss(const void *logits, int dtype, int64_t ld, int T, int E,
                      const int32_t *topk_idx, int K, const uint8_t *valid, int32_t *counts,

@@ -12,6 +12,10 @@
 // Forward: each workgroup keeps its rows' sums of p per column in registers and its counts in LDS
 // and leaves one row of partial sums; a second launch adds those, and its last workgroup (an
 // integer ticket) forms the loss.  All float sums are in an order that depends on the sizes alone.
+//
+// At E = 512 (us): 8192 fp32 rows, forward 6.8, join 4.0, backward 9.2 (17 and 34 MB, which the
+// caches hold: the waits of a row's two reductions bound it); 30118 bf16 rows, a fifth of them
+// invalid, 11.9, 3.9, 18 (backward, with its zero rows: 55 MB, 3.1 TB/s).
 #include <math.h>
 
 #include <type_traits>
@@ -65,7 +69,7 @@ __device__ __forceinline__ float wave_reduce(float v, F f) {
   return f(f(row(0), row(1)), f(row(2), row(3)));
 }
 __device__ __forceinline__ float wave_max(float v) {
-  return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); });
+  return wave_reduce(v, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
 }
 __device__ __forceinline__ float wave_sum(float v) {
   return wave_reduce(v, [](float a, float b) { return a + b; });
@@ -100,13 +104,14 @@ struct Row {
   // exp(x - max) of each column, 0 past E; returns 1 / their sum, or 0 for a row with nothing above
   // -inf.  The exponential is the hardware's 2^t of t = (x - max) log2 e: the roundings of the
   // difference, the product and the constant make |x - max| 2.25 * 2^-24 of it, besides its ulp.
-  // (With expf the kernels were bound by its instructions.)
+  // (With expf the kernels were bound by its instructions.)  The maximum keeps a NaN, so a row that
+  // holds one, or +inf, is NaN throughout and not taken for one with nothing above -inf.
   __device__ __forceinline__ float softmax(float (&p)[VPL]) const {
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
       p[j] = (float)v[j / VEC][j % VEC];
-      m = fmaxf(m, p[j]);
+      m = __builtin_elementwise_maximum(m, p[j]);
     }
     m = wave_max(m);
     const bool none = m == -INFINITY;
@@ -359,7 +364,8 @@ hipError_t backward(const BalanceArgs& a, const int32_t* counts, const float* gr
   const int groups = (a.T + kWaves - 1) / kWaves;
   return dispatch<DT>(a.E, together, [&](auto V, auto W) {
     balance_backward_kernel<DT, decltype(V)::value, decltype(W)::value>
-        <<<groups < kBackwardGroups ? groups : kBackwardGroups, kWaves * 64, 0, s>>>(a, counts, grad_loss, grad, ld);
+        <<<groups < kBackwardGroups ? groups : kBackwardGroups, kWaves * 64, 0, s>>>(
+            a, counts, grad_loss, grad, ld);
   });
 }
 

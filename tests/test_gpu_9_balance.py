@@ -158,3 +158,30 @@ def test_balance_repeats_bit_for_bit():
     for _ in range(3):
         for p, q in zip(a, run(xt, idx, v, 1.0)):
             assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("E", [3, 64, 130, 512])
+def test_balance_of_a_valid_row_without_a_softmax_is_nan(E, dtype):
+    """A NaN among the logits, nothing but NaN, NaN among -inf, +inf: the loss, every mean and that row's
+    gradient are NaN, the counts and the other rows' gradients as without it."""
+    T, K = 20, 2
+    x, idx, v = case(T, E, K, "all", 3 * E)
+    clean = run(dev(x).to(DT[dtype]), idx, v, 2.0)
+    for kind in range(4):
+        y = x.copy()
+        if kind == 0:
+            y[7, E // 2] = np.nan
+        elif kind == 1:
+            y[7] = np.nan
+        elif kind == 2:
+            y[7] = -np.inf
+            y[7, E - 1] = np.nan
+        else:
+            y[7, 0] = np.inf
+        counts, prob, loss, grad = run(dev(y).to(DT[dtype]), idx, v, 2.0)
+        assert torch.equal(counts, clean[0])
+        assert bool(prob.isnan().all()) and bool(loss.isnan().all())
+        assert bool(grad[7].isnan().all())
+        rest = torch.arange(T, device="cuda") != 7
+        assert torch.equal(grad[rest], clean[3][rest])
