@@ -86,10 +86,11 @@ class MoePrefillLayer:
 
 
 class MoeMxfp4Layer:
-    """The layer over experts in MXFP4, held on one GPU: routing, maps, the tokens quantised once, gate/up
-    with SwiGLU and requantisation, down into bf16 rows, combine.  gate_up [E, 2F, H] (gate's F rows,
-    then up's) and down [E, H, F]: floating-point tensors, quantised here once, or (codes, scales)
-    pairs.  H and F: multiples of 128.  A layer's calls share its buffers, so they must not overlap."""
+    """The layer over experts in MXFP4, held on one GPU: routing, maps, the tokens quantised once,
+    gate/up with SwiGLU and requantisation, down into bf16 rows, combine.  gate_up [E, 2F, H]
+    (gate's F rows, then up's) and down [E, H, F]: floating-point tensors, quantised here once, or
+    (codes, scales) pairs.  H and F: multiples of 128.  A layer's calls share its buffers, so they
+    must not overlap."""
 
     def __init__(self, gate_up, down, max_tokens: int, K: int, device="cuda"):
         self.device = torch.device(device)
@@ -100,13 +101,16 @@ class MoeMxfp4Layer:
             raise ValueError("gate_up [E, 2F, H] and down [E, H, F] do not fit each other")
         if self.H % 128 or self.F % 128 or not 1 <= K <= self.E:
             raise ValueError("H and F are multiples of 128, K one of 1 .. E")
+        if max_tokens < 1:
+            raise ValueError("max_tokens is at least 1")
         self.max_tokens, self.K = max_tokens, K
         R = max_tokens * K
         self.counts, self.offsets = self._i32(self.E), self._i32(self.E + 1)
         self.src, self.slot = self._i32(R), self._i32(R)
         self.order, self.n_active = self._i32(self.E), self._i32(1)
         self.maps_ws = self._u8(abi.build_maps_workspace_size(max_tokens, K, self.E))
-        self.x_codes, self.x_scales = self._u8(max_tokens, self.H // 2), self._u8(max_tokens, self.H // 32)
+        self.x_codes = self._u8(max_tokens, self.H // 2)
+        self.x_scales = self._u8(max_tokens, self.H // 32)
         self.h_codes, self.h_scales = self._u8(R, self.F // 2), self._u8(R, self.F // 32)
         self.rows = torch.empty((R, self.H), dtype=torch.bfloat16, device=self.device)
         self.balance_ws = self._u8(abi.balance_workspace_size(max_tokens, self.E))
@@ -126,13 +130,20 @@ class MoeMxfp4Layer:
         abi.mxfp4_quantize(w.view(E * N, k), codes.view(E * N, -1), scales.view(E * N, -1))
         return codes, scales
 
-    def _tokens(self, t: torch.Tensor) -> int:
-        if t.shape[0] > self.max_tokens:
-            raise ValueError(f"T={t.shape[0]} exceeds the buffers' {self.max_tokens} tokens")
-        return t.shape[0]
+    def _tokens(self, t: torch.Tensor, idx: torch.Tensor) -> int:
+        T = t.shape[0]
+        if T > self.max_tokens:
+            raise ValueError(f"T={T} exceeds the buffers' {self.max_tokens} tokens")
+        self._want(("idx", idx, torch.int32, (T, self.K)))
+        return T
+
+    def _want(self, *wants):
+        """Routing and maps take pointers: what they read and write has to fit the layer."""
+        abi._want(abi._on_current(self.src), *wants)
 
     def route(self, logits: torch.Tensor):
         T = logits.shape[0]
+        self._want(("logits", logits, torch.float32, (T, self.E)))
         idx = torch.empty((T, self.K), dtype=torch.int32, device=self.device)
         w = torch.empty((T, self.K), dtype=torch.float32, device=self.device)
         abi.route_topk(logits, self.K, idx, w)
@@ -142,7 +153,7 @@ class MoeMxfp4Layer:
                 grad_loss: torch.Tensor | None = None):
         """The router's counts int32 [E + 1] (the valid tokens last), mean probabilities, balance loss
         and the loss's gradient (times grad_loss) with respect to the logits."""
-        self._tokens(logits)
+        self._tokens(logits, idx)
         counts, prob = self._i32(self.E + 1), torch.empty(self.E, device=self.device)
         loss, grad = torch.empty(1, device=self.device), torch.empty_like(logits)
         abi.balance_loss(logits, idx, counts, prob, loss, self.balance_ws, valid=valid)
@@ -151,7 +162,8 @@ class MoeMxfp4Layer:
 
     def forward(self, x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor,
                 out: torch.Tensor | None = None) -> torch.Tensor:
-        T = self._tokens(x)
+        T = self._tokens(x, idx)
+        self._want(("w", w, torch.float32, (T, self.K)))
         R = T * self.K
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.float32, device=self.device)

@@ -492,3 +492,34 @@ def test_layer_is_the_path():
             layer.step(torch.randn(71, 256, device="cuda"), torch.randn(71, 16, device="cuda"))
     with pytest.raises(ValueError):
         MoeMxfp4Layer(p.gu, p.gu, max_tokens=4, K=2)
+
+
+def test_layer_refuses_what_does_not_fit_it():
+    """Routes and logits of other sizes, types, layouts or devices than the layer's are refused before a
+    launch: the maps would be written past their buffers, or read through a host address."""
+    p = Path(12, 256, 128, 16, 2, 4)
+    layer = MoeMxfp4Layer(p.gu, p.dn, max_tokens=12, K=2)
+    idx, w = layer.route(p.logits)
+    x = p.x
+    more = torch.zeros((13, 2), dtype=torch.int32, device="cuda")
+    wide = torch.zeros((12, 3), dtype=torch.int32, device="cuda")
+    for bad in (more, wide, idx[:11], idx.long(), idx.cpu(), more.repeat(2, 1)[::2][:12], wide[:, :2]):
+        with pytest.raises(ValueError):
+            layer.forward(x, bad, w)
+        with pytest.raises(ValueError):
+            layer.balance(p.logits, bad)
+    for bad in (w[:11], w.double(), w.cpu(), w.T.contiguous().T):
+        with pytest.raises(ValueError):
+            layer.forward(x, idx, bad)
+    for bad in (p.logits[:, :15], p.logits.bfloat16(), p.logits.cpu(), torch.randn(12, 17, device="cuda")):
+        with pytest.raises(ValueError):
+            layer.route(bad)
+    with pytest.raises(ValueError):
+        layer.balance(torch.randn(12, 17, device="cuda"), idx)
+    with pytest.raises(ValueError):
+        layer.forward(x[:, :128], idx, w)
+    with pytest.raises(ValueError):
+        layer.forward(x, idx, w, out=torch.empty(12, 255, device="cuda"))
+    with pytest.raises(ValueError):
+        MoeMxfp4Layer(p.gu, p.dn, max_tokens=0, K=2)
+    assert torch.equal(layer.forward(x, idx, w), layer.step(x, p.logits))
