@@ -86,7 +86,9 @@ hipError_t launch_combine_bf16(const void* rows, const int32_t* slot, const floa
 // Balance loss: workgroups of the forward pass, each leaving one row of partial sums.
 constexpr int kBalanceGroups = 256;
 constexpr int kBalanceHeader = 2048;  // bytes of the workspace before those rows
-inline int balance_groups(int T) { return T < 16 * kBalanceGroups ? (T + 15) / 16 : kBalanceGroups; }
+inline int balance_groups(int T) {
+  return T < 16 * kBalanceGroups ? (T + 15) / 16 : kBalanceGroups;
+}
 struct BalanceArgs {
   const void* logits;
   int dtype;

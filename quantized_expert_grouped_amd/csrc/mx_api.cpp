@@ -10,7 +10,8 @@ namespace {
 
 using namespace moe;
 
-static_assert((int)MOE_F32 == kF32 && (int)MOE_BF16 == kBF16 && (int)MOE_F16 == kF16, "the ABI's types");
+static_assert((int)MOE_F32 == kF32 && (int)MOE_BF16 == kBF16 && (int)MOE_F16 == kF16,
+              "the ABI's types");
 static_assert(MOE_MX_F32 == kMxF32 && MOE_MX_BF16 == kMxBF16 && MOE_MX_SWIGLU_MXFP4 == kMxSwiglu,
               "the ABI's epilogues");
 
@@ -73,12 +74,13 @@ int moe_mxfp4_mm_grouped(const void* w_codes, const void* w_scales, int n_out, i
   if (!src && n_act < rows) return MOE_EINVAL;
   if (n_out % 32 != 0 || k_in % 128 != 0 || E > MOE_MAX_E) return MOE_EUNSUPPORTED;
   if (src && K > MOE_MAX_K) return MOE_EUNSUPPORTED;
-  // tiles are numbered in 31 bits, a grid's y holds 16, and rows are addressed by 32-bit offsets from an
-  // expert's matrix and from a_codes
+  // tiles are numbered in 31 bits, a grid's y holds 16, and rows are addressed by 32-bit offsets
+  // from an expert's matrix and from a_codes
   const int64_t mats = epilogue == MOE_MX_SWIGLU_MXFP4 ? 2 : 1;
   if (rows / 32 + E > kMaxGroups || n_out / 32 > 65535 ||
       ((int64_t)rows / 32 + E) * (n_out / 32) >= (int64_t)1 << 31 ||
-      mats * n_out * (k_in / 2) >= (int64_t)1 << 32 || (int64_t)n_act * (k_in / 2) >= (int64_t)1 << 32)
+      mats * n_out * (k_in / 2) >= (int64_t)1 << 32 ||
+      (int64_t)n_act * (k_in / 2) >= (int64_t)1 << 32)
     return MOE_EUNSUPPORTED;
   if (!aligned(w_codes, 16) || !aligned(a_codes, 16) || !aligned(w_scales, 4) ||
       !aligned(a_scales, 4) || !aligned(out, 16))
@@ -102,8 +104,8 @@ int moe_mxfp4_mm_grouped(const void* w_codes, const void* w_scales, int n_out, i
   return status_of(launch_mx_mm(p, as_stream(stream)));
 }
 
-int moe_combine_bf16(const void* rows, const int32_t* slot, const float* topk_w, int T, int K, int H,
-                     float* out, void* stream) {
+int moe_combine_bf16(const void* rows, const int32_t* slot, const float* topk_w, int T, int K,
+                     int H, float* out, void* stream) {
   if (!rows || !slot || !topk_w || !out || T < 1 || K < 1 || H < 1) return MOE_EINVAL;
   if (!aligned(rows, 16) || !aligned(out, 16)) return MOE_EINVAL;
   if (H % 8 != 0 || K > MOE_MAX_K || (long long)T * K > kMaxRows) return MOE_EUNSUPPORTED;

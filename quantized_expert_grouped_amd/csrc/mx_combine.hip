@@ -14,8 +14,9 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 // A thread owns 8 columns of a token and keeps up to kBatch rows' loads under way (each row is read
-// once: non-temporal); the token's slots and weights are scalars.  Bound by memory: 8192 tokens, K
-// = 10, H = 2048 (403 MB).
+// once: non-temporal); the token's slots and weights are scalars.  Bound by memory: 8192 tokens,
+// K = 10, H = 2048 (403 MB) take 69 to 73 us, 5.5 to 5.9 TB/s; with one row's
+// plain load at a time, 84.
 constexpr int kBatch = 8;
 
 __global__ __launch_bounds__(256) void combine_bf16_kernel(const uint16_t* __restrict__ rows,

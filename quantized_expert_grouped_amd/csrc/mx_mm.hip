@@ -1,5 +1,6 @@
 // The grouped MXFP4 product: row r of expert e is
-//   y[r, n] = sum over blocks b of 2^(ea - 127) 2^(ew - 127) sum_j A[row(r), 32 b + j] W[e, n, 32 b + j],
+//   y[r, n] = sum over blocks b of
+//             2^(ea - 127) 2^(ew - 127) sum_j A[row(r), 32b + j] W[e, n, 32b + j],
 // which v_mfma_scale_f32_32x32x64_f8f6f4 computes whole: e2m1 codes and the blocks' scale bytes go
 // in as they lie in memory, sums stay in fp32.
 //
@@ -42,15 +43,16 @@ __device__ __forceinline__ v16f mfma_mx(const v4i& w, const v4i& a, const v16f& 
 struct Tile {
   int expert, row0, nrows;
 };
-__device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, int E, int rows, int id,
-                                          bool by_row) {
+__device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, int E, int rows,
+                                          int id, bool by_row) {
   constexpr int BM = 32;
   const int lane = threadIdx.x & 63;
   int upto = 0;  // experts whose first number is not above id: a prefix of them
   for (int e0 = 0; e0 < E; e0 += 512) {
     int o[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = e0 + 64 * j < E ? offsets[min(e0 + 64 * j + lane, E - 1)] : 0;
+    for (int j = 0; j < 8; ++j)
+      o[j] = e0 + 64 * j < E ? offsets[min(e0 + 64 * j + lane, E - 1)] : 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int e = e0 + 64 * j + lane;
@@ -77,9 +79,9 @@ __device__ __forceinline__ float swiglu(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
-// ---- few rows ------------------------------------------------------------------------------ One
-// workgroup: up to 32 rows of an expert by 32 columns (SwiGLU: 32 gates and their 32 ups), K split
-// over its 4 wavefronts and joined in LDS.  With so few rows a call is bound by latency: each
+// ---- few rows ------------------------------------------------------------------------------
+// One workgroup: up to 32 rows of an expert by 32 columns (SwiGLU: 32 gates and their 32 ups), K
+// split over its 4 wavefronts and joined in LDS.  With so few rows a call is bound by latency: each
 // wavefront loads its operands from memory straight into the MFMA's layout, with no stage or
 // barrier before the join.  One token's ten rows, gate/up (11 MB of weights): 7.0 us; down: 4.6 us.
 template <int EPI>
@@ -174,7 +176,8 @@ __global__ __launch_bounds__(256) void mx_mm_narrow_kernel(MxProblem p, bool by_
     if (live) {
       uint8_t* o = static_cast<uint8_t*>(p.out) + row * (p.n_out / 2) + (n0 + tc) / 2;
       *reinterpret_cast<uint16_t*>(o) = (uint16_t)codes;
-      if ((threadIdx.x & 7) == 0) p.out_scales[row * (p.n_out / kMxBlock) + n0 / kMxBlock] = (uint8_t)byte;
+      if ((threadIdx.x & 7) == 0)
+        p.out_scales[row * (p.n_out / kMxBlock) + n0 / kMxBlock] = (uint8_t)byte;
     }
   } else if (live) {
     if constexpr (EPI == kMxF32) {
@@ -183,7 +186,8 @@ __global__ __launch_bounds__(256) void mx_mm_narrow_kernel(MxProblem p, bool by_
     } else {
       typedef __bf16 v4 __attribute__((ext_vector_type(4)));
       __bf16* o = static_cast<__bf16*>(p.out) + row * p.n_out + n0 + tc;
-      *reinterpret_cast<v4*>(o) = (v4){(__bf16)y[0][0], (__bf16)y[0][1], (__bf16)y[0][2], (__bf16)y[0][3]};
+      *reinterpret_cast<v4*>(o) =
+          (v4){(__bf16)y[0][0], (__bf16)y[0][1], (__bf16)y[0][2], (__bf16)y[0][3]};
     }
   }
 }
@@ -201,10 +205,12 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // writes a scalar register (a readlane, as it restores spilled scalars) and a load that takes its
 // address from it, 5 wait states: the s_nop does, and covers the one that M0 needs.
 __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" : : "{m0}"(lds), "v"(off), "s"(base) : "memory");
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
+               : : "{m0}"(lds), "v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_nop 4\n\tglobal_load_lds_dword %1, %2" : : "{m0}"(lds), "v"(off), "s"(base) : "memory");
+  asm volatile("s_nop 4\n\tglobal_load_lds_dword %1, %2"
+               : : "{m0}"(lds), "v"(off), "s"(base) : "memory");
 }
 
 // A workgroup's tile: BN weight rows by BM routed rows, its wavefronts in WN slices of the columns
@@ -231,13 +237,17 @@ struct Geo {
 };
 template <class G>
 struct Lds {
-  uint8_t rows[G::NBUF][G::kBuf];          // a stage's weight rows, then its routed rows
-  uint8_t scales[G::NBUF][G::kRows * 16];  // their scale bytes: of 512 values, or of a stage
+  // a stage's weight rows, then its routed rows
+  alignas(16) uint8_t rows[G::NBUF][G::kBuf];
+  // their scale bytes: of 512 values, or of a stage
+  alignas(16) uint8_t scales[G::NBUF][G::kRows * 16];
 };
 
 // Where a row's 16-byte piece c lies among its 8 in LDS: at c ^ swizzle(row).  Lanes of consecutive
 // rows then read one piece index from different banks, in groups of 8 as of 16 lanes.
-__device__ __forceinline__ int swizzle(int row) { return ((row >> 1) & 3) | (((row ^ (row >> 3)) & 1) << 2); }
+__device__ __forceinline__ int swizzle(int row) {
+  return ((row >> 1) & 3) | (((row ^ (row >> 3)) & 1) << 2);
+}
 
 // Waits for the wavefront's loads to LDS, and for its LDS reads: what it read may be overwritten
 // after the barrier.
@@ -255,18 +265,22 @@ struct Dma {
   static constexpr int kScales = WIDE ? G::kSI : G::kS4I;
   const uint8_t *w, *ws, *a, *as;
   uint32_t wo[G::kWI], ao[G::kAI], so[kScales];
+  __device__ static int s_load(int i, int wave) {
+    return WIDE ? min(wave + G::kWaves * i, G::kS - 1) : min(wave + G::kWaves * i, G::kS4 - 1);
+  }
   __device__ static bool s_is_w(int i, int wave) {  // whether scale load i is of weight rows
-    return WIDE ? min(wave + G::kWaves * i, G::kS - 1) < G::BN / 64 : min(wave + G::kWaves * i, G::kS4 - 1) < G::BN / 32;
+    return WIDE ? s_load(i, wave) < G::BN / 64 : s_load(i, wave) < G::BN / 32;
   }
   // the tile row of a lane in scale load i, and its byte there
   __device__ static int s_row(int i, int wave, int lane) {
-    return WIDE ? 64 * min(wave + G::kWaves * i, G::kS - 1) + lane : 32 * min(wave + G::kWaves * i, G::kS4 - 1) + lane / 2;
+    return WIDE ? 64 * s_load(i, wave) + lane : 32 * s_load(i, wave) + lane / 2;
   }
   __device__ static int s_byte(int lane) { return WIDE ? 0 : 4 * (lane & 1); }
 };
 
 template <class G, bool WIDE, class WR>
-__device__ __forceinline__ void plan_weights(Dma<G, WIDE>& d, int k_in, WR wrow, int wave, int lane) {
+__device__ __forceinline__ void plan_weights(Dma<G, WIDE>& d, int k_in, WR wrow, int wave,
+                                             int lane) {
   const uint32_t kb = k_in / 2, sb = k_in / kMxBlock;
 #pragma unroll
   for (int i = 0; i < G::kWI; ++i) {
@@ -300,8 +314,8 @@ __device__ __forceinline__ void plan_rows(Dma<G, WIDE>& d, int k_in, AR arow, in
 // `last_half`: of a last stage of 128 values, whose pieces 4..7 (scale bytes 4..7) do not exist;
 // those lanes load the first ones again, and the products leave them out.
 template <class G, bool WIDE>
-__device__ __forceinline__ void issue_row(const Dma<G, WIDE>& d, int i, int stage, uint32_t rows, bool last_half,
-                                          int wave, int lane) {
+__device__ __forceinline__ void issue_row(const Dma<G, WIDE>& d, int i, int stage, uint32_t rows,
+                                          bool last_half, int wave, int lane) {
   const size_t k = (size_t)stage * kStage;
   auto off = [&](uint32_t o, int row) {
     if (WIDE || !last_half) return o;
@@ -316,15 +330,16 @@ __device__ __forceinline__ void issue_row(const Dma<G, WIDE>& d, int i, int stag
   }
 }
 template <class G, bool WIDE>
-__device__ __forceinline__ void issue_scales(const Dma<G, WIDE>& d, int stage, uint32_t scales, bool last_half, int wave, int lane) {
+__device__ __forceinline__ void issue_scales(const Dma<G, WIDE>& d, int stage, uint32_t scales,
+                                             bool last_half, int wave, int lane) {
   const size_t k = (size_t)stage * 8;
 #pragma unroll
   for (int i = 0; i < d.kScales; ++i) {
     const uint8_t* base = (d.s_is_w(i, wave) ? d.ws : d.as) + k;
     if (WIDE)
-      dma16(base, d.so[i], scales + 1024 * min(wave + G::kWaves * i, G::kS - 1));
+      dma16(base, d.so[i], scales + 1024 * d.s_load(i, wave));
     else
-      dma4(base, d.so[i] - (last_half ? d.s_byte(lane) : 0), scales + 256 * min(wave + G::kWaves * i, G::kS4 - 1));
+      dma4(base, d.so[i] - (last_half ? d.s_byte(lane) : 0), scales + 256 * d.s_load(i, wave));
   }
 }
 
@@ -355,11 +370,13 @@ __device__ __forceinline__ Reads plan_reads(const Lds<G>& lds, int wn, int wm, i
 // to a half of a stage's time if it issues them in a row), so load(i), i < LOADS, are spread over
 // the products, which go on meanwhile.
 template <class G, bool WIDE, int NL, int LOADS, class F>
-__device__ __forceinline__ void products(const Reads& r, int rows_at, int scales_at, v16f (&acc)[G::TN][G::TM],
-                                         bool last_half, int lane, F load) {
+__device__ __forceinline__ void products(const Reads& r, int rows_at, int scales_at,
+                                         v16f (&acc)[G::TN][G::TM], bool last_half, int lane,
+                                         F load) {
   constexpr int kStride = WIDE ? 16 : 8;
   constexpr int N = NL > 0 ? NL : 1;
-  const bool none = !WIDE && last_half && lane >= 32;  // this lane's blocks do not exist: codes 0 at scale 1
+  // this lane's blocks do not exist: codes 0 at scale 1
+  const bool none = !WIDE && last_half && lane >= 32;
   if constexpr (NL == 0) {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) load(i);
@@ -389,10 +406,11 @@ __device__ __forceinline__ void products(const Reads& r, int rows_at, int scales
         for (int q = 0; q < 4; ++q) o.w[j][q] = none ? 0 : o.w[j][q];
     }
 #pragma unroll
-    for (int i = 0; i < NL; ++i) o.a[i] = *reinterpret_cast<const v4i*>(r.a[s] + rows_at + i * G::WM * 32 * kStage);
+    for (int i = 0; i < NL; ++i)
+      o.a[i] = *reinterpret_cast<const v4i*>(r.a[s] + rows_at + i * G::WM * 32 * kStage);
     return o;
   };
-  constexpr int kSpread = 2 * N * G::TN;  // over the first half of them: they have to land by the next stage
+  constexpr int kSpread = 2 * N * G::TN;  // the first half of them: they land by the next stage
   Operands now = read(0);
   auto step = [&](auto S) {
     constexpr int s = decltype(S)::value;
@@ -406,7 +424,8 @@ __device__ __forceinline__ void products(const Reads& r, int rows_at, int scales
         const int m = (s * NL + i) * G::TN + j;
         if (LOADS > 0 && m <= kSpread) {
 #pragma unroll
-          for (int l = m * LOADS / kSpread; l < (m + 1) * LOADS / kSpread && l < LOADS; ++l) load(l);
+          for (int l = m * LOADS / kSpread; l < LOADS && l < (m + 1) * LOADS / kSpread; ++l)
+            load(l);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -428,8 +447,9 @@ __device__ __forceinline__ int here(int v) {
 // The wavefront's results for one row tile (32 rows from row0, `live` of them real) to memory.
 // fp32 and bf16 tiles are turned in 4 KiB of LDS, so that 8 lanes write 128 bytes of a row.
 template <class G, int EPI>
-__device__ __forceinline__ void store_tile(const MxProblem& p, const v16f (&acc)[G::TN][G::TM], int i, size_t row0,
-                                           int live, int n0, uint8_t* turn, int lane) {
+__device__ __forceinline__ void store_tile(const MxProblem& p, const v16f (&acc)[G::TN][G::TM],
+                                           int i, size_t row0, int live, int n0, uint8_t* turn,
+                                           int lane) {
   const int l32 = lane & 31, half = lane >> 5;
   if constexpr (EPI == kMxSwiglu) {
 #pragma unroll
@@ -450,8 +470,9 @@ __device__ __forceinline__ void store_tile(const MxProblem& p, const v16f (&acc)
       if (l32 < live && half == 0) {
         const size_t row = row0 + l32;
         uint8_t* o = static_cast<uint8_t*>(p.out) + row * (p.n_out / 2) + n / 2;
-        *reinterpret_cast<uint4*>(o) = make_uint4((c0 & 0xffffu) | (o0 << 16), (c0 >> 16) | (o0 & 0xffff0000u),
-                                                  (c1 & 0xffffu) | (o1 << 16), (c1 >> 16) | (o1 & 0xffff0000u));
+        *reinterpret_cast<uint4*>(o) =
+            make_uint4((c0 & 0xffffu) | (o0 << 16), (c0 >> 16) | (o0 & 0xffff0000u),
+                       (c1 & 0xffffu) | (o1 << 16), (c1 >> 16) | (o1 & 0xffff0000u));
         p.out_scales[row * (p.n_out / kMxBlock) + n / kMxBlock] = (uint8_t)byte;
       }
     }
@@ -470,19 +491,23 @@ __device__ __forceinline__ void store_tile(const MxProblem& p, const v16f (&acc)
           const int byte = (32 * j + 8 * g + 4 * half) * kSize;
           uint8_t* o = turn + l32 * 128 + 16 * ((byte / 16) ^ (l32 & 7)) + byte % 16;
           if constexpr (EPI == kMxF32)
-            *reinterpret_cast<float4*>(o) = make_float4(y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]);
+            *reinterpret_cast<float4*>(o) =
+                make_float4(y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]);
           else
             *reinterpret_cast<v4b*>(o) =
-                (v4b){(__bf16)y[4 * g], (__bf16)y[4 * g + 1], (__bf16)y[4 * g + 2], (__bf16)y[4 * g + 3]};
+                (v4b){(__bf16)y[4 * g], (__bf16)y[4 * g + 1], (__bf16)y[4 * g + 2],
+                      (__bf16)y[4 * g + 3]};
         }
       }
       const int n = n0 + j0 * 32 + (lane & 7) * (16 / kSize);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int r = 8 * k + lane / 8;
-        const uint4 v = *reinterpret_cast<const uint4*>(turn + r * 128 + 16 * ((lane & 7) ^ (r & 7)));
+        const uint4 v =
+            *reinterpret_cast<const uint4*>(turn + r * 128 + 16 * ((lane & 7) ^ (r & 7)));
         if (r < live && n < p.n_out)
-          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + ((row0 + r) * p.n_out + n) * kSize) = v;
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) +
+                                    ((row0 + r) * p.n_out + n) * kSize) = v;
       }
     }
   }
@@ -495,8 +520,9 @@ struct Ring {
 };
 
 template <class G, bool WIDE>
-__device__ __forceinline__ void issue_stage_scales(const Dma<G, WIDE>& d, int k, bool last_half, Ring& ring, uint32_t lscales,
-                                                   int wave, int lane) {
+__device__ __forceinline__ void issue_stage_scales(const Dma<G, WIDE>& d, int k, bool last_half,
+                                                   Ring& ring, uint32_t lscales, int wave,
+                                                   int lane) {
   if (WIDE && (k & 1) != 0) return;
   ring.loaded = (ring.loaded + 1) & (G::NBUF - 1);
   issue_scales(d, k, lscales + ring.loaded * G::kRows * 16, last_half, wave, lane);
@@ -507,9 +533,10 @@ __device__ __forceinline__ void issue_stage_scales(const Dma<G, WIDE>& d, int k,
 // its last stage issues the first of the next tile, which `turn_over` puts in place of this one in
 // d.
 template <class G, bool WIDE, int NL, class F, class A>
-__device__ __forceinline__ void main_loop(const Reads& r, Dma<G, WIDE>& d, Ring& ring, uint32_t lrows,
-                                          uint32_t lscales, v16f (&acc)[G::TN][G::TM], int k_in, F between, A turn_over,
-                                          int wave, int lane) {
+__device__ __forceinline__ void main_loop(const Reads& r, Dma<G, WIDE>& d, Ring& ring,
+                                          uint32_t lrows, uint32_t lscales,
+                                          v16f (&acc)[G::TN][G::TM], int k_in, F between,
+                                          A turn_over, int wave, int lane) {
   constexpr int kLoads = G::kWI + G::kAI;
   const int stages = (k_in + 255) / 256;
   auto half_stage = [&](int k) { return !WIDE && 256 * (k + 1) > k_in; };
@@ -532,9 +559,10 @@ __device__ __forceinline__ void main_loop(const Reads& r, Dma<G, WIDE>& d, Ring&
       const int kn = k + 1 < stages ? k + 1 : 0;
       if (kn == 0) turn_over();
       issue_stage_scales(d, kn, half_stage(kn), ring, lscales, wave, lane);
-      products<G, WIDE, NL, kLoads>(r, ring.buf * G::kBuf, scales_at, acc, half_stage(k), lane, [&](int i) {
-        issue_row(d, i, kn, lrows + (ring.buf ^ 1) * G::kBuf, half_stage(kn), wave, lane);
-      });
+      products<G, WIDE, NL, kLoads>(
+          r, ring.buf * G::kBuf, scales_at, acc, half_stage(k), lane, [&](int i) {
+            issue_row(d, i, kn, lrows + (ring.buf ^ 1) * G::kBuf, half_stage(kn), wave, lane);
+          });
       if (kAfter) between();
       if (k + 1 < stages) ring.buf ^= 1;
     } else {
@@ -559,7 +587,8 @@ __device__ __forceinline__ int scan(int v) {
 // products of the one at work go on.  (With a workgroup to a pair those two took 5.8 of its 20.6 us
 // at 8192 tokens, 512 experts, gate/up.)
 template <class G, int EPI, bool WIDE>
-__global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kernel(MxProblem p, uint32_t n_tiles) {
+__global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kernel(
+    MxProblem p, uint32_t n_tiles) {
   __shared__ Lds<G> lds;
   constexpr bool kSwiglu = EPI == kMxSwiglu;
   constexpr int kFeat = kSwiglu ? G::BN / 2 : G::BN;  // output columns of a tile
@@ -610,7 +639,8 @@ __global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kerne
       const int mine = lane < seg && u.expert + lane < p.E ? tiles_of(n) : 0;
       const int incl = scan(mine);
       const int s = __popcll(ballot(incl <= u.row0));  // lanes all of whose tiles come before
-      const int m = u.row0 - (__builtin_amdgcn_readlane(incl, s) - __builtin_amdgcn_readlane(mine, s));
+      const int m = u.row0 -
+                    (__builtin_amdgcn_readlane(incl, s) - __builtin_amdgcn_readlane(mine, s));
       const int rows = __builtin_amdgcn_readlane(n, s), count = __builtin_amdgcn_readlane(mine, s);
       // an expert's tiles are equally high, to 32 rows
       const int high = ((rows + count - 1) / count + 31) / 32 * 32;
@@ -630,7 +660,7 @@ __global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kerne
       };
       plan_rows<G, WIDE, false>(e, p.k_in, act, wave, here(lane));
       auto wrow = [&](int i) -> uint32_t {  // the expert's matrix row in row i of the tile
-        if constexpr (kSwiglu) {  // of a wavefront's TN tiles the first half are gates, the others their ups
+        if constexpr (kSwiglu) {  // half of a wavefront's TN tiles are gates, then their ups
           const int tile = i >> 5, slice = tile / G::TN, j = tile % G::TN;
           const int f = un0 + (slice * (G::TN / 2) + j % (G::TN / 2)) * 32 + (i & 31);
           return min(f, p.n_out - 1) + (j >= G::TN / 2 ? p.n_out : 0);
@@ -665,7 +695,7 @@ __global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kerne
     auto between = [&]() {
       if (next < end) advance(next);
     };
-    auto turn_over = [&]() {  // after the last pair its first stage is loaded once more, for nothing
+    auto turn_over = [&]() {  // after the last pair its first stage is loaded again, for nothing
       if (next >= end) return;
       while (at < 3) advance(next);
       d = e;
@@ -683,8 +713,9 @@ __global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kerne
           for (int i = 0; i < NL; ++i)
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[j][i][q] = 0.0f;
-        main_loop<G, WIDE, NL>(r, d, ring, lrows, lscales, acc, p.k_in, between, turn_over, wave, lane);
-        if (!kSwiglu) {  // tiles are turned in the stage's buffer once every wavefront is done with it
+        main_loop<G, WIDE, NL>(r, d, ring, lrows, lscales, acc, p.k_in, between, turn_over, wave,
+                               lane);
+        if (!kSwiglu) {  // tiles are turned in the stage's buffer once all are done with it
           asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
           __builtin_amdgcn_s_barrier();
           asm volatile("" : : : "memory");
@@ -692,8 +723,9 @@ __global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kerne
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
           const int r0 = __builtin_amdgcn_readfirstlane(here((i * G::WM + wm) * 32));
-          store_tile<G, EPI>(p, acc, i, (size_t)t.row0 + r0, min(t.nrows - r0, 32), n0 + wn * (kFeat / G::WN),
-                             lds.rows[ring.buf] + 4096 * wave, here(lane));
+          store_tile<G, EPI>(p, acc, i, (size_t)t.row0 + r0, min(t.nrows - r0, 32),
+                             n0 + wn * (kFeat / G::WN), lds.rows[ring.buf] + 4096 * wave,
+                             here(lane));
         }
       }
     };

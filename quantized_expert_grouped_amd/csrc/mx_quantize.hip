@@ -2,7 +2,8 @@
 //
 // Both kernels move each byte once and are bound by memory.  A lane owns 8 values: 16 or 32 bytes
 // in, one dword of codes, so a block of 32 is a quad of lanes whose largest magnitude takes two DPP
-// steps.
+// steps.  8192 x 2048 values: fp32 quantised in 11 to 12 us (76 MB, 6.4 TB/s, partly
+// from the caches), dequantised to bf16 in 9 to 10 us (42 MB, 4.2 TB/s).
 #include "mx.hpp"
 
 namespace moe {
@@ -55,7 +56,8 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* __restrict
 // code -> its value, as the high 16 bits of an fp32
 __device__ __forceinline__ float mx_value(uint32_t code, float scale) {
   const uint32_t e = (code >> 1) & 3u, mant = code & 1u;
-  const float mag = e == 0 ? 0.5f * (float)mant : __uint_as_float(((e + 126u) << 23) | (mant << 22));
+  const float mag =
+      e == 0 ? 0.5f * (float)mant : __uint_as_float(((e + 126u) << 23) | (mant << 22));
   return ((code & 8u) ? -mag : mag) * scale;
 }
 
