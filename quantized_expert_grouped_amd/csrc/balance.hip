@@ -13,9 +13,9 @@
 // and leaves one row of partial sums; a second launch adds those, and its last workgroup (an
 // integer ticket) forms the loss.  All float sums are in an order that depends on the sizes alone.
 //
-// At E = 512 (us): 8192 fp32 rows, forward 6.8, join 4.0, backward 9.2 (17 and 34 MB, which the
-// caches hold: the waits of a row's two reductions bound it); 30118 bf16 rows, a fifth of them
-// invalid, 11.9, 3.9, 18 (backward, with its zero rows: 55 MB, 3.1 TB/s).
+// At E = 512 (us): 8192 fp32 rows, forward 6.4, join 4.2, backward 7.6 (17 and 34 MB, 4.5 TB/s;
+// starts and the waits of a row's reductions bound it); 30118 bf16 rows, a fifth of them invalid,
+// 11.0, 3.9, 12.5 (backward, with its zero rows: 55 MB, 4.4 TB/s).
 #include <math.h>
 
 #include <type_traits>
@@ -27,8 +27,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kWaves = 16;             // wavefronts of a workgroup
-constexpr int kBackwardGroups = 256;   // one to a CU
+constexpr int kWaves = 16;  // wavefronts of a workgroup
+// of the backward pass, whose wavefronts share nothing (256 of 16: 500 rows 4.6 us instead of 3.0)
+constexpr int kBackwardWaves = 4, kBackwardGroups = 1024;
 
 // Workspace: ticket, each joining workgroup's part of the loss, then per workgroup valid tokens,
 // counts [E], sums [E].
@@ -115,15 +116,26 @@ struct Row {
     }
     m = wave_max(m);
     const bool none = m == -INFINITY;
+    const float from = none ? 0.0f : m;
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      p[j] = none ? 0.0f : __builtin_amdgcn_exp2f((p[j] - m) * 1.44269504088896341f);
+      p[j] = __builtin_amdgcn_exp2f((p[j] - from) * 1.44269504088896341f);
       s += p[j];
     }
     return none ? 0.0f : __builtin_amdgcn_rcpf(wave_sum(s));
   }
 };
+
+// Bit l: row t + l * step is there and valid.  64 rows of a wavefront in one load: with a load per
+// row, which the row's own has to wait for, its latency was a row's longest part.  t and step are
+// uniform; t + 64 * step stays far below 2^31.
+__device__ __forceinline__ uint64_t valid_rows(const BalanceArgs& a, int t, int step, int lane) {
+  const int u = t + lane * step;
+  bool on = u < a.T;
+  if (on && a.valid) on = a.valid[u] != 0;
+  return ballot(on);
+}
 
 template <int DT, int VPL, int VEC>
 __global__ __launch_bounds__(kWaves * 64) void balance_rows_kernel(BalanceArgs a, void* ws) {
@@ -131,25 +143,30 @@ __global__ __launch_bounds__(kWaves * 64) void balance_rows_kernel(BalanceArgs a
   __shared__ int32_t hist[kCols];
   __shared__ float half[kWaves / 2][kCols];
   __shared__ int32_t tokens;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Partials q = partials(ws, gridDim.x, a.E);
-  const int64_t step = (int64_t)gridDim.x * kWaves;
-  int64_t t = (int64_t)blockIdx.x * kWaves + wave;
-  // the first row from t on that is valid (uniform)
-  auto valid_from = [&](int64_t u) {
-    while (u < a.T && a.valid && a.valid[u] == 0) u += step;
+  const int step = gridDim.x * kWaves;
+  int first = blockIdx.x * kWaves + wave;
+  uint64_t left = valid_rows(a, first, step, lane);
+  auto next_row = [&]() {  // the next valid row, or T
+    while (left == 0 && first + 64 * step < a.T) {
+      first += 64 * step;
+      left = valid_rows(a, first, step, lane);
+    }
+    const int u = left ? first + __builtin_ctzll(left) * step : a.T;
+    left &= left - 1;
     return u;
   };
   Row<DT, VPL, VEC> row;
   int32_t id = -1;
-  auto fetch = [&]() {
-    if (t < a.T) {
-      row.load(a.logits, t * a.ld, a.E, lane);
-      if (lane < a.K) id = a.idx[t * a.K + lane];
+  auto fetch = [&](int u) {
+    if (u < a.T) {
+      row.load(a.logits, u * a.ld, a.E, lane);
+      if (lane < a.K) id = a.idx[(int64_t)u * a.K + lane];
     }
   };
-  t = valid_from(t);
-  fetch();
+  int t = next_row();
+  fetch(t);
   for (int e = threadIdx.x; e < kCols; e += kWaves * 64) hist[e] = 0;
   if (threadIdx.x == 0) {
     tokens = 0;
@@ -163,8 +180,8 @@ __global__ __launch_bounds__(kWaves * 64) void balance_rows_kernel(BalanceArgs a
   while (t < a.T) {
     const Row<DT, VPL, VEC> now = row;
     const int32_t e = id;
-    t = valid_from(t + step);
-    fetch();
+    t = next_row();
+    fetch(t);
     ++mine;
     if (lane < a.K && e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
     float p[VPL];
@@ -264,59 +281,72 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(int E, int K, int gr
   }
 }
 
+constexpr int kWaitLoads = 0x0f70;  // s_waitcnt vmcnt(0)
 template <int DT, int VPL, int VEC>
-__global__ __launch_bounds__(kWaves * 64) void balance_backward_kernel(
+__global__ __launch_bounds__(kBackwardWaves * 64) void balance_backward_kernel(
     BalanceArgs a, const int32_t* __restrict__ counts, const float* __restrict__ grad_loss,
     void* __restrict__ grad, int64_t ld_grad) {
   typedef Row<DT, VPL, VEC> R;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t step = (int64_t)gridDim.x * kWaves;
-  int64_t t = (int64_t)blockIdx.x * kWaves + wave;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int step = gridDim.x * kBackwardWaves;
+  int t = blockIdx.x * kBackwardWaves + wave, i64 = 0;
+  uint64_t valid = valid_rows(a, t, step, lane);
   R row;
   bool on = false;
   auto fetch = [&]() {
-    on = t < a.T && (!a.valid || a.valid[t] != 0);  // uniform
+    on = t < a.T && (valid >> i64 & 1);
     if (on) row.load(a.logits, t * a.ld, a.E, lane);
   };
   fetch();
   const int n = counts[a.E];
-  int32_t c[VPL];
+  typedef int32_t ivec __attribute__((ext_vector_type(VEC), aligned(4)));
+  ivec c[VPL / VEC];
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    c[j] = 0;
-    if (column<VEC>(j, lane) < a.E) c[j] = counts[column<VEC>(j, lane)];
+  for (int i = 0; i < VPL / VEC; ++i) {
+    c[i] = (ivec)0;
+    if (column<VEC>(i * VEC, lane) < a.E)
+      c[i] = *reinterpret_cast<const ivec*>(counts + column<VEC>(i * VEC, lane));
   }
-  // g (E / n) (f - 1/E) = g (c E - n K) / (n n K)
+  // g (E / n) (f - 1/E) = g (c E - n K) / (n n K); below 2^53, so exact in fp64, whose one fma takes
+  // an eighth of the 64-bit integers' instructions
   const float nf = (float)n;
   const float scale =
       n > 0 ? (grad_loss ? *grad_loss : 1.0f) / (nf * (float)a.K) / nf : 0.0f;
   float dev[VPL];
 #pragma unroll
   for (int j = 0; j < VPL; ++j)
-    dev[j] = (float)((int64_t)c[j] * a.E - (int64_t)n * a.K) * scale;
+    dev[j] = (float)fma((double)c[j / VEC][j % VEC], (double)a.E, -((double)n * a.K)) * scale;
   while (t < a.T) {
     const R now = row;
     const bool live = on;
     typename R::T* g = static_cast<typename R::T*>(grad) + t * ld_grad;
     t += step;
+    i64 = (i64 + 1) & 63;
+    if (i64 == 0 && t < a.T) valid = valid_rows(a, t, step, lane);
     fetch();
-    float p[VPL], r = 0.0f, dot = 0.0f;
+    float y[VPL];
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) p[j] = 0.0f;
+    for (int j = 0; j < VPL; ++j) y[j] = 0.0f;
     if (live) {
-      r = now.softmax(p);
+      const float r = now.softmax(y);
+      float dot = 0.0f;
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) dot = fmaf(p[j], dev[j], dot);
+      for (int j = 0; j < VPL; ++j) dot = fmaf(y[j], dev[j], dot);
       dot = wave_sum(dot) * r;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) y[j] = y[j] * r * (dev[j] - dot);
     }
+    // the next row's loads before the stores, which would be waited for with them otherwise
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);
 #pragma unroll
     for (int i = 0; i < VPL / VEC; ++i) {
       const int e = column<VEC>(i * VEC, lane);
-      typename R::vec v;
+      typedef float fvec __attribute__((ext_vector_type(VEC)));
+      fvec f;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        v[j] = (typename R::T)(live ? p[i * VEC + j] * r * (dev[i * VEC + j] - dot) : 0.0f);
-      if (e < a.E) *reinterpret_cast<typename R::vec*>(g + e) = v;
+      for (int j = 0; j < VEC; ++j) f[j] = y[i * VEC + j];
+      if (e < a.E)
+        *reinterpret_cast<typename R::vec*>(g + e) = __builtin_convertvector(f, typename R::vec);
     }
   }
 }
@@ -361,10 +391,10 @@ template <int DT>
 hipError_t backward(const BalanceArgs& a, const int32_t* counts, const float* grad_loss, void* grad,
                     int64_t ld, hipStream_t s) {
   const bool together = rows_aligned(a.logits, a.ld, a.dtype) && rows_aligned(grad, ld, a.dtype);
-  const int groups = (a.T + kWaves - 1) / kWaves;
+  const int groups = (a.T + kBackwardWaves - 1) / kBackwardWaves;
   return dispatch<DT>(a.E, together, [&](auto V, auto W) {
     balance_backward_kernel<DT, decltype(V)::value, decltype(W)::value>
-        <<<groups < kBackwardGroups ? groups : kBackwardGroups, kWaves * 64, 0, s>>>(
+        <<<groups < kBackwardGroups ? groups : kBackwardGroups, kBackwardWaves * 64, 0, s>>>(
             a, counts, grad_loss, grad, ld);
   });
 }

@@ -185,3 +185,19 @@ def test_balance_of_a_valid_row_without_a_softmax_is_nan(E, dtype):
         assert bool(grad[7].isnan().all())
         rest = torch.arange(T, device="cuda") != 7
         assert torch.equal(grad[rest], clean[3][rest])
+
+
+@pytest.mark.parametrize("gap", [False, True])
+def test_balance_of_more_rows_than_the_wavefronts_see_at_once(gap):
+    """More than 64 rows to each of the largest grid's wavefronts, all valid and with runs of invalid rows
+    that are longer than what one wavefront looks ahead."""
+    T, E, K = 2 * 64 * 4096 + 777, 4, 2
+    x, idx, _ = case(T, E, K, "all", 21)
+    v = None
+    if gap:
+        v = np.zeros(T, np.uint8)
+        v[5::7001] = 1
+        v[-700:] = 255
+        v[70000:70100] = 3
+    xt = dev(x)
+    check(xt, idx, v, "float32", 1e3, run(xt, idx, v, 1e3))
