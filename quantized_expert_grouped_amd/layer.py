@@ -89,7 +89,8 @@ class MoeMxfp4Layer:
     """The layer over experts in MXFP4, held on one GPU: routing, maps, the tokens quantised once,
     gate/up with SwiGLU and requantisation, down into bf16 rows, combine.  gate_up [E, 2F, H]
     (gate's F rows, then up's) and down [E, H, F]: floating-point tensors, quantised here once, or
-    (codes, scales) pairs.  H and F: multiples of 128.  A layer's calls share its buffers, so they
+    pairs of codes (uint8 or float4_e2m1fn_x2 [E, rows, k / 2]) and scales (uint8 or float8_e8m0fnu
+    [E, rows, k / 32]).  H and F: multiples of 128.  A layer's calls share its buffers, so they
     must not overlap."""
 
     def __init__(self, gate_up, down, max_tokens: int, K: int, device="cuda"):
@@ -123,7 +124,14 @@ class MoeMxfp4Layer:
 
     def _weights(self, w):
         if isinstance(w, (tuple, list)):
-            return tuple(_to_device(t, torch.uint8, self.device) for t in w)
+            codes, scales = w
+            codes = _mx_bytes("codes", codes, torch.float4_e2m1fn_x2, self.device)
+            scales = _mx_bytes("scales", scales, torch.float8_e8m0fnu, self.device)
+            E, N, kb = codes.shape
+            if scales.shape != (E, N, kb // 16) or kb % 16:
+                raise ValueError(f"scales: {(E, N, kb // 16)} are wanted for codes {(E, N, kb)}, "
+                                 f"not {tuple(scales.shape)}")
+            return codes, scales
         w = w.to(self.device).contiguous()
         E, N, k = w.shape
         codes, scales = self._u8(E, N, k // 2), self._u8(E, N, k // 32)
@@ -183,6 +191,15 @@ class MoeMxfp4Layer:
         """One pass of the whole path: routing, then the layer."""
         idx, w = self.route(logits)
         return self.forward(x, idx, w, out)
+
+
+def _mx_bytes(name: str, a, own, device) -> torch.Tensor:
+    """MXFP4's codes or scales as bytes on the device: uint8, or torch's own type for them, whose bytes
+    they are.  (A conversion would take a scale of 0.5 for the byte 0.)"""
+    t = a if isinstance(a, torch.Tensor) else torch.from_numpy(np.ascontiguousarray(a))
+    if t.dtype not in (torch.uint8, own):
+        raise ValueError(f"{name}: uint8 or {own} is wanted, not {t.dtype}")
+    return t.view(torch.uint8).to(device).contiguous()
 
 
 def _to_device(a, dtype, device):

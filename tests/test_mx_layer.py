@@ -1,0 +1,72 @@
+"""What MoeMxfp4Layer takes and refuses when it is made (CPU only: its buffers are host tensors here and no
+call reaches a kernel)."""
+import numpy as np
+import pytest
+import torch
+
+from quantized_expert_grouped_amd.layer import MoeMxfp4Layer
+
+E, H, F = 3, 256, 128
+
+
+def pairs(seed=0):
+    g = torch.Generator().manual_seed(seed)
+
+    def rand(*shape):
+        return torch.randint(0, 256, shape, dtype=torch.uint8, generator=g)
+
+    return ((rand(E, 2 * F, H // 2), rand(E, 2 * F, H // 32)), (rand(E, H, F // 2), rand(E, H, F // 32)))
+
+
+def make(gate_up, down, max_tokens=4, K=2):
+    return MoeMxfp4Layer(gate_up, down, max_tokens=max_tokens, K=K, device="cpu")
+
+
+def test_weights_in_bytes_or_in_torchs_types_for_them():
+    """float8_e8m0fnu scales and float4_e2m1fn_x2 codes are taken as the bytes they are, in any layout."""
+    gate_up, down = pairs()
+    want = make(gate_up, down)
+    for t, b in zip(want.gate_up + want.down, gate_up + down):
+        assert t.dtype == torch.uint8 and torch.equal(t, b)
+
+    def typed(p):
+        return p[0].view(torch.float4_e2m1fn_x2), p[1].view(torch.float8_e8m0fnu)
+
+    def turned(p):                                            # the same values, strides the other way
+        return tuple(t.transpose(0, 2).contiguous().transpose(0, 2) for t in p)
+
+    def arrays(p):
+        return [t.numpy() for t in p]
+
+    for form in (typed, turned, arrays):
+        got = make(form(gate_up), form(down))
+        for t, b in zip(got.gate_up + got.down, gate_up + down):
+            assert t.dtype == torch.uint8 and t.is_contiguous() and torch.equal(t, b), form
+    scales = torch.tensor([0.125, 0.5, 1.0, 8.0]).to(torch.float8_e8m0fnu).repeat(E * 2 * F * 2)
+    got = make((gate_up[0], scales.view(E, 2 * F, H // 32)), down).gate_up[1]
+    assert got[0, 0].tolist() == [124, 126, 127, 130] * 2
+
+
+def test_weights_that_are_not_bytes_are_refused():
+    gate_up, down = pairs()
+    (gc, gs), (dc, ds) = gate_up, down
+    for bad in ((gc.int(), gs), (gc.view(torch.int8), gs), (gc.float(), gs), (gc, gs.float()),
+                (gc, gs.int()), (gc, gs.view(torch.int8)), (gc, gs.bfloat16()),
+                (gc, gs.view(torch.float8_e4m3fn)), (gc.view(torch.float8_e8m0fnu), gs),
+                (gc, gs.view(torch.float4_e2m1fn_x2)), (gc.numpy().astype(np.int64), gs)):
+        with pytest.raises(ValueError):
+            make(bad, down)
+    with pytest.raises(ValueError):
+        make(gate_up, (dc, ds.float()))
+
+
+def test_weights_whose_scales_do_not_fit_are_refused():
+    gate_up, down = pairs()
+    (gc, gs), (dc, ds) = gate_up, down
+    for bad in ((gc, gs[..., :-1]), (gc, gs[:-1]), (gc, gs[:, :F]), (gc, gs.flatten(1)), (gc[:-1], gs),
+                (gc.flatten(1), gs), (gc, gs, gs), (gc[..., :120], gs[..., :7])):
+        with pytest.raises(ValueError):
+            make(bad, down)
+    for bad in ((dc, ds[..., :2]), (dc, ds[:, :-32]), gate_up):
+        with pytest.raises(ValueError):
+            make(gate_up, bad)
