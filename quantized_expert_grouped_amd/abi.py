@@ -20,6 +20,7 @@ QUANT_PER_ROW, QUANT_D4 = 1, 2
 EPI_F32, EPI_SWIGLU_Q8_1, EPI_I32_BLOCKDOTS = 0, 1, 2
 F32, BF16, F16 = 0, 1, 2
 MX_F32, MX_BF16, MX_SWIGLU_MXFP4 = 0, 1, 2
+MAX_E, MAX_K = 2048, 64
 WS_COUNTS, WS_OFFSETS, WS_SRC, WS_SLOT, WS_ORDER, WS_NACTIVE, WS_Q8X, WS_GROUPS, WS_HQ8, WS_DM, \
     WS_GROUP_STRIDE, WS_STATUS = range(12)
 N_STAGES = 6

@@ -100,8 +100,10 @@ class MoeMxfp4Layer:
         self.H, self.F = 2 * hb, f2 // 2
         if self.down[0].shape != (self.E, self.H, self.F // 2) or f2 % 2:
             raise ValueError("gate_up [E, 2F, H] and down [E, H, F] do not fit each other")
-        if self.H % 128 or self.F % 128 or not 1 <= K <= self.E:
-            raise ValueError("H and F are multiples of 128, K one of 1 .. E")
+        if self.H % 128 or self.F % 128 or not 1 <= K <= min(self.E, abi.MAX_K):
+            raise ValueError(f"H and F are multiples of 128, K one of 1 .. E, {abi.MAX_K} at most")
+        if self.E > abi.MAX_E:
+            raise ValueError(f"E={self.E} exceeds {abi.MAX_E}")
         if max_tokens < 1:
             raise ValueError("max_tokens is at least 1")
         self.max_tokens, self.K = max_tokens, K

@@ -1,9 +1,13 @@
 """What MoeMxfp4Layer takes and refuses when it is made (CPU only: its buffers are host tensors here and no
 call reaches a kernel)."""
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
 
+from quantized_expert_grouped_amd import abi
 from quantized_expert_grouped_amd.layer import MoeMxfp4Layer
 
 E, H, F = 3, 256, 128
@@ -70,3 +74,20 @@ def test_weights_whose_scales_do_not_fit_are_refused():
     for bad in ((dc, ds[..., :2]), (dc, ds[:, :-32]), gate_up):
         with pytest.raises(ValueError):
             make(gate_up, bad)
+
+
+def test_more_experts_or_routes_than_the_library_takes_are_refused():
+    text = open(os.path.join(os.path.dirname(__file__), "..", "include", "moe_prefill.h")).read()
+    for name, value in (("MOE_MAX_E", abi.MAX_E), ("MOE_MAX_K", abi.MAX_K)):
+        assert int(re.search(rf"#define {name} (\d+)", text).group(1)) == value
+
+    def layer(n, K):
+        u8 = torch.uint8
+        return MoeMxfp4Layer((torch.zeros(n, 256, 64, dtype=u8), torch.zeros(n, 256, 4, dtype=u8)),
+                             (torch.zeros(n, 128, 64, dtype=u8), torch.zeros(n, 128, 4, dtype=u8)),
+                             max_tokens=2, K=K, device="cpu")
+
+    assert layer(abi.MAX_E, abi.MAX_K).K == abi.MAX_K
+    for n, K in ((abi.MAX_E + 1, 2), (80, abi.MAX_K + 1), (3, 4), (3, 0)):
+        with pytest.raises(ValueError):
+            layer(n, K)
