@@ -164,8 +164,8 @@ class MoeMxfp4Layer:
         """The router's counts int32 [E + 1] (the valid tokens last), mean probabilities, balance loss
         and the loss's gradient (times grad_loss) with respect to the logits."""
         self._tokens(logits, idx)
-        counts, prob = self._i32(self.E + 1), torch.empty(self.E, device=self.device)
-        loss, grad = torch.empty(1, device=self.device), torch.empty_like(logits)
+        counts, grad = self._i32(self.E + 1), torch.empty_like(logits)
+        prob, loss = (torch.empty(n, dtype=torch.float32, device=self.device) for n in (self.E, 1))
         abi.balance_loss(logits, idx, counts, prob, loss, self.balance_ws, valid=valid)
         abi.balance_loss_backward(logits, counts, self.K, grad, valid=valid, grad_loss=grad_loss)
         return counts, prob, loss, grad

@@ -91,3 +91,24 @@ def test_more_experts_or_routes_than_the_library_takes_are_refused():
     for n, K in ((abi.MAX_E + 1, 2), (80, abi.MAX_K + 1), (3, 4), (3, 0)):
         with pytest.raises(ValueError):
             layer(n, K)
+
+
+@pytest.mark.parametrize("default", [torch.float32, torch.bfloat16, torch.float64])
+def test_balance_makes_its_outputs_in_the_types_the_library_takes(default, monkeypatch):
+    """Whatever torch's default type is.  The library's calls are replaced: their arguments are looked at."""
+    layer = make(*pairs())
+    seen = []
+    monkeypatch.setattr(abi, "_on_current", lambda t: t.get_device())
+    monkeypatch.setattr(abi, "balance_loss", lambda *a, **k: seen.extend(a))
+    monkeypatch.setattr(abi, "balance_loss_backward", lambda *a, **k: seen.extend(a))
+    logits, idx = torch.zeros(4, E, dtype=torch.float16), torch.zeros(4, 2, dtype=torch.int32)
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(default)
+    try:
+        counts, prob, loss, grad = layer.balance(logits, idx)
+    finally:
+        torch.set_default_dtype(before)
+    assert seen[2] is counts and seen[3] is prob and seen[4] is loss and seen[-1] is grad
+    assert (counts.dtype, prob.dtype, loss.dtype) == (torch.int32, torch.float32, torch.float32)
+    assert (counts.shape, prob.shape, loss.shape) == ((E + 1,), (E,), (1,))
+    assert grad.dtype == torch.float16 and grad.shape == logits.shape
