@@ -177,12 +177,16 @@ class MoeMxfp4Layer:
         R = T * self.K
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.float32, device=self.device)
+        else:
+            self._want(("out", out, torch.float32, (T, self.H)))
+            if out.data_ptr() % 16:
+                raise ValueError("out: an address that is a multiple of 16 is wanted")
         src, slot, rows = self.src[:R], self.slot[:R], self.rows[:R]
         x_codes, x_scales = self.x_codes[:T], self.x_scales[:T]
         h_codes, h_scales = self.h_codes[:R], self.h_scales[:R]
+        abi.mxfp4_quantize(x, x_codes, x_scales)  # first: it looks x over
         abi.build_maps(idx, self.E, 0, self.counts, self.offsets, src, slot, self.order,
                        self.n_active, self.maps_ws)
-        abi.mxfp4_quantize(x, x_codes, x_scales)
         abi.mxfp4_mm_grouped(*self.gate_up, self.offsets, x_codes, x_scales, h_codes, src=src,
                              K=self.K, out_scales=h_scales)
         abi.mxfp4_mm_grouped(*self.down, self.offsets, h_codes, h_scales, rows)

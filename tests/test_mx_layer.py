@@ -112,3 +112,28 @@ def test_balance_makes_its_outputs_in_the_types_the_library_takes(default, monke
     assert (counts.dtype, prob.dtype, loss.dtype) == (torch.int32, torch.float32, torch.float32)
     assert (counts.shape, prob.shape, loss.shape) == ((E + 1,), (E,), (1,))
     assert grad.dtype == torch.float16 and grad.shape == logits.shape
+
+
+def test_forward_refuses_x_and_out_before_it_enqueues_anything(monkeypatch):
+    layer = make(*pairs())
+    done = []
+    monkeypatch.setattr(abi, "_on_current", lambda t: t.get_device())
+    monkeypatch.setattr(abi, "_current_stream", lambda stream, device: 0)
+    for name in ("build_maps", "mxfp4_mm_grouped", "combine_bf16"):
+        monkeypatch.setattr(abi, name, lambda *a, _name=name, **k: done.append(_name))
+    real = abi.mxfp4_quantize
+    monkeypatch.setattr(abi, "mxfp4_quantize", lambda *a: (real(*a), done.append("mxfp4_quantize")))
+    idx, w = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    x = torch.zeros(4, H)
+    apart = torch.zeros(4 * (H + 8))
+    for bad in (x[:, :128], torch.zeros(4, 2 * H), torch.zeros(4, H + 32), torch.zeros(4, H + 1), x.double(),
+                x.int(), x.t().contiguous().t(), x[0].expand(4, H), apart[1:1 + 4 * H].view(4, H),
+                torch.zeros(4, H + 1)[:, :H]):
+        with pytest.raises((ValueError, abi.MoeError)):
+            layer.forward(bad, idx, w)
+        assert not done
+    for bad in (torch.zeros(4, H - 1), torch.zeros(5, H), torch.zeros(4, H).bfloat16(),
+                torch.zeros(4, 2 * H)[:, :H], apart[1:1 + 4 * H].view(4, H)):
+        with pytest.raises(ValueError):
+            layer.forward(x, idx, w, out=bad)
+        assert not done
