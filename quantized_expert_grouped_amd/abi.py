@@ -435,8 +435,12 @@ def _row_stride(name: str, t, device: int) -> int:
 
 
 def _current_stream(stream, device: int):
-    # torch.cuda.current_stream() builds a Stream object, 2.8 us of a call that takes 6
-    return _torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    # torch.cuda.current_stream() builds a Stream object, 2.8 us of a call that takes 6; the raw one
+    # comes from a private function, which a torch may not have
+    if stream is not None:
+        return _stream(stream)
+    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+    return _stream(None) if raw is None else raw(device)
 
 
 def mxfp4_quantize(x, codes, scales, stream=None):

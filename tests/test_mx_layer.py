@@ -137,3 +137,16 @@ def test_forward_refuses_x_and_out_before_it_enqueues_anything(monkeypatch):
         with pytest.raises(ValueError):
             layer.forward(x, idx, w, out=bad)
         assert not done
+
+
+def test_the_current_stream_without_torchs_private_function(monkeypatch):
+    class Stream:
+        cuda_stream = 0x1230
+
+    abi._dtypes()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0x4560 + device, raising=False)
+    assert abi._current_stream(None, 2) == 0x4562
+    assert abi._current_stream(Stream, 0) == 0x1230 and abi._current_stream(7, 0) == 7
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    assert abi._current_stream(None, 0) == 0x1230
