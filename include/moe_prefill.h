@@ -61,7 +61,10 @@
 extern "C" {
 #endif
 
+/* MOE_ABI_VERSION goes up when something that was there changes, MOE_ABI_MINOR when entry points
+ * are added to it.  7.1: moe_abi_minor, moe_mxfp4_*, moe_combine_bf16, moe_balance_*. */
 #define MOE_ABI_VERSION 7
+#define MOE_ABI_MINOR 1
 #define MOE_MAX_GROUP 16     /* experts per group buffer ([G1] "What": MMQ_GROUP = 16) */
 #define MOE_MAX_E 2048       /* largest expert count the kernels accept */
 #define MOE_MAX_K 64         /* largest routes per token */
@@ -97,6 +100,7 @@ typedef enum {
 } moe_epilogue;
 
 int moe_abi_version(void);
+int moe_abi_minor(void);     /* a library that lacks it is one of minor 0 */
 const char *moe_strerror(int status);
 
 /* Sizes (bytes). */

@@ -41,6 +41,7 @@ STATUS = {0: "MOE_OK", -1: "MOE_EINVAL", -2: "MOE_EUNSUPPORTED", -3: "MOE_EWORKS
 P, I, SZ, L64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
 SIGNATURES = {
     "moe_abi_version": (I, []),
+    "moe_abi_minor": (I, []),
     "moe_strerror": (ctypes.c_char_p, [I]),
     "moe_block_bytes": (SZ, [I]),
     "moe_expert_bytes": (SZ, [I, I, I]),
@@ -95,6 +96,10 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m quantized_expert_grouped_amd.build`")
         L = ctypes.CDLL(LIB_PATH)
+        lacks = [name for name in SIGNATURES if not hasattr(L, name)]
+        if lacks:
+            raise RuntimeError(f"{LIB_PATH} is older than this binding and lacks {', '.join(lacks)}: "
+                               "build it with `python -m quantized_expert_grouped_amd.build`")
         for name, (res, args) in SIGNATURES.items():
             fn = getattr(L, name)
             fn.restype = res
@@ -128,6 +133,10 @@ def _check(name: str, rc: int) -> None:
 # ---- sizes ----------------------------------------------------------------------------------
 def abi_version() -> int:
     return lib().moe_abi_version()
+
+
+def abi_minor() -> int:
+    return lib().moe_abi_minor()
 
 
 def strerror(status: int) -> str:

@@ -32,6 +32,7 @@ void destroy_events() {
 extern "C" {
 
 int moe_abi_version(void) { return MOE_ABI_VERSION; }
+int moe_abi_minor(void) { return MOE_ABI_MINOR; }
 
 const char* moe_strerror(int status) {
   switch (status) {
