@@ -114,7 +114,7 @@ int moe_combine_bf16(const void* rows, const int32_t* slot, const float* topk_w,
 }
 
 size_t moe_balance_workspace_size(int T, int E) {
-  if (T < 1 || E < 1 || E > MOE_MAX_E) return 0;
+  if (T < 1 || T > kMaxRows || E < 1 || E > MOE_MAX_E) return 0;
   return (size_t)kBalanceHeader + (size_t)balance_groups(T) * E * 8;
 }
 
