@@ -489,7 +489,8 @@ int moe_balance_loss(const void *logits, int dtype, int64_t ld, int T, int E,
 /* Its gradient (f is a constant of it, the counts having none):
  *   grad_logits[t, j] = g (E/n) p[t, j] (f[j] - sum_e f[e] p[t, e]),
  * g = grad_loss[0] (device fp32; NULL: 1), rounded once to `dtype`; 0 for an invalid token.
- * counts: as moe_balance_loss left them.  grad_logits may be logits itself. */
+ * counts: as moe_balance_loss left them.  grad_logits may be logits itself,
+ * with ld_grad = ld then; it may not overlap them otherwise. */
 int moe_balance_loss_backward(const void *logits, int dtype, int64_t ld, int T, int E,
                               const int32_t *counts, int K, const uint8_t *valid,
                               const float *grad_loss, void *grad_logits, int64_t ld_grad,

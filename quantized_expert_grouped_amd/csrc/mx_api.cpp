@@ -138,6 +138,8 @@ int moe_balance_loss_backward(const void* logits, int dtype, int64_t ld, int T, 
   const int rc = check_balance(logits, dtype, ld, T, E, K);
   if (rc != MOE_OK) return rc;
   if (T > 1 && ld_grad < E) return MOE_EINVAL;
+  // in place a row's gradient may be written before another row is read
+  if (T > 1 && grad_logits == logits && ld_grad != ld) return MOE_EINVAL;
   if (!aligned(grad_logits, (size_t)size_of(dtype))) return MOE_EINVAL;
   const BalanceArgs a{logits, dtype, ld, T, E, K, nullptr, valid};
   return status_of(launch_balance_backward(a, counts, grad_loss, grad_logits, ld_grad,

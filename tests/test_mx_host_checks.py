@@ -10,3 +10,10 @@ def test_balance_workspace_of_more_tokens_than_the_call_takes():
         assert abi.balance_workspace_size(T, 8) == 0
         p = 1 << 20
         assert abi.lib().moe_balance_loss(p, 0, 8, T, 8, p, 1, None, p, p, p, p, 1 << 30, None) == -2
+
+
+def test_balance_gradient_over_its_logits_with_other_strides():
+    p = 1 << 20
+    bwd = abi.lib().moe_balance_loss_backward
+    for ld, ld_grad in ((64, 72), (72, 64)):
+        assert bwd(p, 0, ld, 100, 64, p, 4, None, None, p, ld_grad, None) == -1
