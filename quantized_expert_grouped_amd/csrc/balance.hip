@@ -76,6 +76,8 @@ __device__ __forceinline__ float wave_sum(float v) {
   return wave_reduce(v, [](float a, float b) { return a + b; });
 }
 
+constexpr float kLog2E = 1.44269504088896341f;
+
 // A lane's VPL columns of a row: VEC neighbours, then VEC neighbours 64 VEC further on, ...
 template <int VEC>
 __device__ __forceinline__ int column(int j, int lane) {
@@ -102,11 +104,14 @@ struct Row {
       if (c < E) v[i] = *reinterpret_cast<const vec*>(l + c);
     }
   }
-  // exp(x - max) of each column, 0 past E; returns 1 / their sum, or 0 for a row with nothing above
-  // -inf.  The exponential is the hardware's 2^t of t = (x - max) log2 e: the roundings of the
-  // difference, the product and the constant make |x - max| 2.25 * 2^-24 of it, besides its ulp.
-  // (With expf the kernels were bound by its instructions.)  The maximum keeps a NaN, so a row that
-  // holds one, or +inf, is NaN throughout and not taken for one with nothing above -inf.
+  // exp(x - max) of each column times a factor near 1 that the row shares, 0 past E; returns 1 /
+  // their sum, or 0 for a row with nothing above -inf.  The exponential is the hardware's 2^t of t =
+  // x log2 e - c in one fma, c = max log2 e rounded once for the whole row (its rounding, below
+  // 2^-8, is the factor).  So of a probability's error |x - max| 2^-24 is t's one rounding and a
+  // quarter of that the constant's, besides 2^t's ulp; forming x - max first would round twice.  From
+  // |max| = 2^16 on c's rounding could carry 2^t out of range, and x - max is formed first.  (With expf
+  // the kernels were bound by its instructions.)  The maximum keeps a NaN, so a row that holds one, or
+  // +inf, is NaN throughout and not taken for one with nothing above -inf.
   __device__ __forceinline__ float softmax(float (&p)[VPL]) const {
     float m = -INFINITY;
 #pragma unroll
@@ -116,14 +121,25 @@ struct Row {
     }
     m = wave_max(m);
     const bool none = m == -INFINITY;
-    const float from = none ? 0.0f : m;
     float s = 0.0f;
+    if (fabsf(m) < 65536.0f) {  // uniform
+      const float c = m * kLog2E;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      p[j] = __builtin_amdgcn_exp2f((p[j] - from) * 1.44269504088896341f);
-      s += p[j];
+      for (int j = 0; j < VPL; ++j) {
+        p[j] = __builtin_amdgcn_exp2f(fmaf(p[j], kLog2E, -c));
+        s += p[j];
+      }
+    } else {
+      const float from = none ? 0.0f : m;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        p[j] = __builtin_amdgcn_exp2f((p[j] - from) * kLog2E);
+        s += p[j];
+      }
     }
-    return none ? 0.0f : __builtin_amdgcn_rcpf(wave_sum(s));
+    s = wave_sum(s);
+    const float r = __builtin_amdgcn_rcpf(s);  // 1 ulp; a Newton step leaves little more than half
+    return none ? 0.0f : fmaf(r, fmaf(-s, r, 1.0f), r);
   }
 };
 
