@@ -441,7 +441,8 @@ typedef enum {
     MOE_MX_F32 = 0,           /* out = fp32 [rows x n_out] */
     MOE_MX_BF16 = 1,          /* out = bf16 [rows x n_out], rounded once from the fp32 sums */
     MOE_MX_SWIGLU_MXFP4 = 2   /* out = codes, out_scales = scales of h = silu(gate) * up, rows of
-                                 n_out values quantised as moe_mxfp4_quantize does */
+                                 n_out values quantised as moe_mxfp4_quantize does; silu is 0
+                                 where it is less than 2^-119 in magnitude (gates below -87.3) */
 } moe_mx_epilogue;
 
 /* The grouped product over every expert in one call: for expert e and its rows r = offsets[e] ..

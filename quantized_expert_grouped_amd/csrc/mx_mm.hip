@@ -72,8 +72,10 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, i
   return t;
 }
 
-// silu(g) * u in fp32 with the hardware's exponential and reciprocal, 1 ulp each; the rounding of
-// the exponent's argument adds |g| 2^-24.  g far below zero gives g * (1 / inf) = -0.
+// silu(g) * u in fp32 with the hardware's exponential and reciprocal, 1 ulp each; the roundings of
+// the exponent's argument and of its constant add 1.25 |g| 2^-24.  The result goes into 4 bits.
+// From g = -87.4 down 1 + e is 2^126 or more, whose reciprocal the hardware takes for 0: the result
+// is -0 where silu(g) is less than 2^-119 in magnitude.
 __device__ __forceinline__ float swiglu(float g, float u) {
   const float e = __builtin_amdgcn_exp2f(g * -1.44269504088896341f);
   return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
