@@ -87,13 +87,18 @@ class MoePrefillLayer:
 
 class MoeMxfp4Layer:
     """The layer over experts in MXFP4, held on one GPU: routing, maps, the tokens quantised once,
-    gate/up with SwiGLU and requantisation, down into bf16 rows, combine.  gate_up [E, 2F, H]
+    gate/up with SwiGLU and requantisation, down into rows of rows_dtype, combine.  bfloat16 rows
+    are half the bytes (at long prompts fp32 ones are more than all weights) and one rounding,
+    2^-8 of a value; float32 rows none.  gate_up [E, 2F, H]
     (gate's F rows, then up's) and down [E, H, F]: floating-point tensors, quantised here once, or
     pairs of codes (uint8 or float4_e2m1fn_x2 [E, rows, k / 2]) and scales (uint8 or float8_e8m0fnu
     [E, rows, k / 32]).  H and F: multiples of 128.  A layer's calls share its buffers, so they
     must not overlap."""
 
-    def __init__(self, gate_up, down, max_tokens: int, K: int, device="cuda"):
+    def __init__(self, gate_up, down, max_tokens: int, K: int, device="cuda",
+                 rows_dtype: torch.dtype = torch.bfloat16):
+        if rows_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"rows_dtype: bfloat16 or float32 is wanted, not {rows_dtype}")
         self.device = torch.device(device)
         self.gate_up, self.down = self._weights(gate_up), self._weights(down)
         self.E, f2, hb = self.gate_up[0].shape
@@ -115,7 +120,7 @@ class MoeMxfp4Layer:
         self.x_codes = self._u8(max_tokens, self.H // 2)
         self.x_scales = self._u8(max_tokens, self.H // 32)
         self.h_codes, self.h_scales = self._u8(R, self.F // 2), self._u8(R, self.F // 32)
-        self.rows = torch.empty((R, self.H), dtype=torch.bfloat16, device=self.device)
+        self.rows = torch.empty((R, self.H), dtype=rows_dtype, device=self.device)
         self.balance_ws = self._u8(abi.balance_workspace_size(max_tokens, self.E))
 
     def _u8(self, *shape):
@@ -190,7 +195,8 @@ class MoeMxfp4Layer:
         abi.mxfp4_mm_grouped(*self.gate_up, self.offsets, x_codes, x_scales, h_codes, src=src,
                              K=self.K, out_scales=h_scales)
         abi.mxfp4_mm_grouped(*self.down, self.offsets, h_codes, h_scales, rows)
-        abi.combine_bf16(rows, slot, w, out)
+        combine = abi.combine_bf16 if rows.dtype == torch.bfloat16 else abi.combine
+        combine(rows, slot, w, out)
         return out
 
     def step(self, x: torch.Tensor, logits: torch.Tensor, out: torch.Tensor | None = None):

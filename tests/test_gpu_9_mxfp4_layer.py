@@ -48,11 +48,12 @@ def same(a, b):
     return all(np.array_equal(p, q) for p, q in zip(a, b, strict=True))
 
 
-@pytest.mark.parametrize("T,H,F,E,K", SIZES)
-def test_layer_against_the_reference(T, H, F, E, K):
+@pytest.mark.parametrize("T,H,F,E,K,options", [(*s, {}) for s in SIZES] + [
+    (*SIZES[0], dict(rows_dtype=torch.float32)), (1, 512, 384, 16, 4, dict(rows_dtype=torch.float32))])
+def test_layer_against_the_reference(T, H, F, E, K, options):
     """Each stage against the reference applied to the stage before it as the GPU left it."""
-    c = Case(T, H, F, E, K, T, max_tokens=T + 13)
-    note(f"MoeMxfp4Layer T={T} H={H} F={F} E={E} K={K}")
+    c = Case(T, H, F, E, K, T, max_tokens=T + 13, **options)
+    note(f"MoeMxfp4Layer T={T} H={H} F={F} E={E} K={K} {options}")
     out, idx, w, counts = c.run()[:4]
     la, R = c.layer, T * K
     off, src, slot = host(la.offsets), host(la.src)[:R], host(la.slot)[:R]
@@ -69,8 +70,10 @@ def test_layer_against_the_reference(T, H, F, E, K):
     hc, hs = host(la.h_codes)[:R], host(la.h_scales)[:R]
     mxref.check_codes(hc, hs, h, dh)
     y2, s2 = mxref.grouped(mxref.decode(hc, hs), mxref.decode(*c.dn), off)
+    assert la.rows.dtype == options.get("rows_dtype", torch.bfloat16)
+    half = 2.0 ** -8 if la.rows.dtype == torch.bfloat16 else 0.0
     rows = exact_f64(la.rows[:R])
-    assert np.all(np.abs(rows - y2) <= sum_bound(F, s2) * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(y2))
+    assert np.all(np.abs(rows - y2) <= sum_bound(F, s2) * (1 + half) + half * np.abs(y2))
     own = host(w).astype(np.float64)[..., None] * rows[slot.reshape(T, K)]
     assert np.all(np.abs(exact_f64(out) - own.sum(1)) <= K * 2.0 ** -24 * np.abs(own).sum(1))
 

@@ -150,3 +150,14 @@ def test_the_current_stream_without_torchs_private_function(monkeypatch):
     assert abi._current_stream(Stream, 0) == 0x1230 and abi._current_stream(7, 0) == 7
     monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
     assert abi._current_stream(None, 0) == 0x1230
+
+
+def test_the_rows_type_is_the_callers_choice():
+    gate_up, down = pairs()
+    assert make(gate_up, down).rows.dtype == torch.bfloat16
+    for t in (torch.bfloat16, torch.float32):
+        layer = MoeMxfp4Layer(gate_up, down, max_tokens=4, K=2, device="cpu", rows_dtype=t)
+        assert layer.rows.dtype == t and layer.rows.shape == (8, H)
+    for t in (torch.float16, torch.float64, torch.uint8):
+        with pytest.raises(ValueError):
+            MoeMxfp4Layer(gate_up, down, max_tokens=4, K=2, device="cpu", rows_dtype=t)
