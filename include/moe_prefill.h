@@ -431,8 +431,9 @@ int moe_mxfp4_quantize(const void *x, int dtype, int64_t ldx, int rows, int n, v
                        void *scales, void *stream);
 
 /* The values that codes and scales stand for: y [rows x n] in MOE_F32 or MOE_BF16 (MOE_F16, whose
- * range is smaller, is refused), rows ldy values apart.  Exact, but for 4 and 6 times 2^127, which
- * are infinite.  Alignment as above. */
+ * range is smaller, is refused), rows ldy values apart.  Exact, but for values of 2^128 and more (2,
+ * 3, 4, 6 times 2^127 and 4, 6 times 2^126, scales that moe_mxfp4_quantize never gives), which are
+ * infinite.  Alignment as above. */
 int moe_mxfp4_dequantize(const void *codes, const void *scales, int rows, int n, void *y,
                          int dtype, int64_t ldy, void *stream);
 
@@ -455,7 +456,7 @@ typedef enum {
  * on are left as they were.  An a(r) outside [0, n_act) is a caller error that stays in bounds:
  * the row nearest is read.  The order of the fp32 sums depends on the sizes alone.
  * codes and out 16-byte aligned, scales 4-byte (else MOE_EINVAL; 16-byte aligned scales are faster
- * where k_in is a multiple of 512).  MOE_EUNSUPPORTED: n_out not a multiple of 32 or above 2^21,
+ * where k_in is a multiple of 512).  MOE_EUNSUPPORTED: n_out not a multiple of 32 or from 2^21 on,
  * k_in not one of 128, E > MOE_MAX_E, K > MOE_MAX_K, an expert's codes or a_codes of 4 GiB or more,
  * rows above 2^28 - 32 E, (rows / 32 + E) (n_out / 32) of 2^31 or more. */
 int moe_mxfp4_mm_grouped(const void *w_codes, const void *w_scales, int n_out, int k_in,
@@ -479,7 +480,8 @@ int moe_combine_bf16(const void *rows, const int32_t *slot, const float *topk_w,
  * A logit of -inf is an expert the token may not take; a valid token with nothing else has p = 0 and
  * counts in n.  NaN or +inf in a valid row makes p[t] NaN, and with it prob_mean, the loss and the
  * row's gradient (an invalid row is not looked at).  Sums are in fp32 and in an order that depends
- * on the sizes alone: the same call gives the same bits.  logits: `dtype` values [T x E], rows ld values apart (ld >= E).
+ * on the sizes and on which rows are valid, not on addresses or strides: the same values give the
+ * same bits.  logits: `dtype` values [T x E], rows ld values apart (ld >= E).
  * ws: moe_balance_workspace_size(T, E) bytes, 4-byte aligned.  E <= MOE_MAX_E,
  * K <= min(E, MOE_MAX_K). */
 size_t moe_balance_workspace_size(int T, int E);   /* 0 for sizes the call would refuse */

@@ -11,11 +11,13 @@
 // meanwhile (-inf: an expert that the token may not take; a row of nothing else has p = 0).
 // Forward: each workgroup keeps its rows' sums of p per column in registers and its counts in LDS
 // and leaves one row of partial sums; a second launch adds those, and its last workgroup (an
-// integer ticket) forms the loss.  All float sums are in an order that depends on the sizes alone.
+// integer ticket) forms the loss.  All float sums are in an order that depends on the sizes and the
+// valid rows alone.
 //
-// At E = 512 (us): 8192 fp32 rows, forward 6.4, join 4.2, backward 7.6 (17 and 34 MB, 4.5 TB/s;
-// starts and the waits of a row's reductions bound it); 30118 bf16 rows, a fifth of them invalid,
-// 11.0, 3.9, 12.5 (backward, with its zero rows: 55 MB, 4.4 TB/s).
+// At E = 512 (us by the kernel trace, which adds a kernel's start): 8192 fp32 rows, forward 6.4, join
+// 4.5, backward 7.5 (17 and 34 MB, 4.5 TB/s; starts and the waits of a row's reductions bound it);
+// 30118 bf16 rows, a fifth of them invalid, 10.4, 4.5, 12.7 (backward, with its zero rows: 55 MB,
+// 4.4 TB/s).  40 calls in one graph: forward with join 9.5 and 13.8, backward 6.6 and 12.0.
 #include <math.h>
 
 #include <type_traits>
@@ -28,7 +30,7 @@ namespace moe {
 namespace {
 
 constexpr int kWaves = 16;  // wavefronts of a workgroup
-// of the backward pass, whose wavefronts share nothing (256 of 16: 500 rows 4.6 us instead of 3.0)
+// of the backward pass, whose wavefronts share nothing (256 of 16: 500 rows 4.6 us instead of 2.7)
 constexpr int kBackwardWaves = 4, kBackwardGroups = 1024;
 
 // Workspace: ticket, each joining workgroup's part of the loss, then per workgroup valid tokens,

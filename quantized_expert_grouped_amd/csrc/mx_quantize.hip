@@ -53,7 +53,7 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* __restrict
   if ((threadIdx.x & 3) == 0) scales[at / kMxBlock] = (uint8_t)byte;
 }
 
-// code -> its value, as the high 16 bits of an fp32
+// code -> its value times the block's scale
 __device__ __forceinline__ float mx_value(uint32_t code, float scale) {
   const uint32_t e = (code >> 1) & 3u, mant = code & 1u;
   const float mag =
