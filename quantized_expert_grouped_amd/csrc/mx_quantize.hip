@@ -3,7 +3,7 @@
 // Both kernels move each byte once and are bound by memory.  A lane owns 8 values: 16 or 32 bytes
 // in, one dword of codes, so a block of 32 is a quad of lanes whose largest magnitude takes two DPP
 // steps.  8192 x 2048 values: fp32 quantised in 11 to 12 us (76 MB, 6.4 TB/s, partly
-// from the caches), dequantised to bf16 in 9 to 10 us (42 MB, 4.2 TB/s).
+// from the caches), dequantised to bf16 in 9 to 11 us (42 MB, 4.2 TB/s).
 #include "mx.hpp"
 
 namespace moe {

@@ -178,14 +178,12 @@ class MoeMxfp4Layer:
     def forward(self, x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor,
                 out: torch.Tensor | None = None) -> torch.Tensor:
         T = self._tokens(x, idx)
-        self._want(("w", w, torch.float32, (T, self.K)))
+        self._want(("w", w, torch.float32, (T, self.K)), ("out", out, torch.float32, (T, self.H)))
         R = T * self.K
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.float32, device=self.device)
-        else:
-            self._want(("out", out, torch.float32, (T, self.H)))
-            if out.data_ptr() % 16:
-                raise ValueError("out: an address that is a multiple of 16 is wanted")
+        elif out.data_ptr() % 16:
+            raise ValueError("out: an address that is a multiple of 16 is wanted")
         src, slot, rows = self.src[:R], self.slot[:R], self.rows[:R]
         x_codes, x_scales = self.x_codes[:T], self.x_scales[:T]
         h_codes, h_scales = self.h_codes[:R], self.h_scales[:R]
