@@ -134,3 +134,45 @@ def test_routes_out_of_range_add_nothing():
     own = np.where(on[..., None], host(w).astype(np.float64)[..., None] * rows[np.maximum(slot, 0)], 0.0)
     assert np.all(np.abs(out - own.sum(1)) <= c.K * 2.0 ** -24 * np.abs(own).sum(1))
     assert int(host(c.layer.offsets)[c.E]) == on.sum()
+
+
+@pytest.mark.parametrize("T,H,F,E,K", [(37, 256, 128, 8, 3), SIZES[0], (5, 128, 128, 1, 1), (600, 128, 256, 1, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_tokens_of_each_type_in_rows_with_gaps(T, H, F, E, K, dtype):
+    """x as every second row of a wider matrix, and into an out of the caller's: the bytes of the contiguous
+    call.  One expert for all tokens among the sizes."""
+    c = Case(T, H, F, E, K, 6)
+    whole = torch.full((2 * T, H + 16), 7.0, device="cuda", dtype=dtype)
+    x = whole[::2, 8:8 + H]
+    x.copy_(c.x)
+    idx, w = c.layer.route(c.logits)
+    want = c.layer.forward(x.contiguous(), idx, w).clone()
+    out = torch.full((T + 1, H), 5.0, device="cuda")
+    assert c.layer.forward(x, idx, w, out=out[:T]).data_ptr() == out.data_ptr()
+    assert torch.equal(out[:T], want) and bool((out[T] == 5.0).all())
+    ec, es = mxref.encode(exact_f64(x))
+    assert np.array_equal(host(c.layer.x_codes)[:T], ec) and np.array_equal(host(c.layer.x_scales)[:T], es)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_balance_of_padded_logits_in_rows_with_gaps(dtype):
+    c = Case(*SIZES[0], 7)
+    whole = torch.full((c.T, c.E + 5), 7.0, device="cuda", dtype=dtype)
+    logits = whole[:, 3:3 + c.E]
+    logits.copy_(c.logits)
+    idx, _ = c.layer.route(c.logits)
+    valid = (torch.arange(c.T, device="cuda") % 5 != 2).to(torch.uint8)
+    g = torch.full((1,), 64.0, device="cuda")
+    want = c.layer.balance(logits.contiguous(), idx, valid=valid, grad_loss=g)
+    for a, b in zip(c.layer.balance(logits, idx, valid=valid, grad_loss=g), want, strict=True):
+        assert torch.equal(a, b)
+    counts, prob, loss, grad = want
+    n = int(valid.sum())
+    ref = mxref.balance(exact_f64(logits), host(idx), host(valid))
+    assert np.array_equal(host(counts), ref[0]) and int(counts[c.E]) == n
+    assert abs(float(loss) - ref[2]) <= 1e-5 * ref[2]
+    assert grad.dtype == dtype and bool((grad[valid == 0] == 0).all())
+    one = c.layer.balance(logits, idx, valid=valid)[3]                # without grad_loss: 1
+    # 64 is a power of two: the same roundings but where a value is subnormal
+    tiny = torch.finfo(dtype).tiny
+    assert bool(((grad.double() - 64 * one.double()).abs() <= 64 * tiny).all())
