@@ -62,9 +62,10 @@ extern "C" {
 #endif
 
 /* MOE_ABI_VERSION goes up when something that was there changes, MOE_ABI_MINOR when entry points
- * are added to it.  7.1: moe_abi_minor, moe_mxfp4_*, moe_combine_bf16, moe_balance_*. */
+ * are added to it.  7.1: moe_abi_minor, moe_mxfp4_*, moe_combine_bf16, moe_balance_*.
+ * 7.2: moe_dispatch_rows, moe_combine_rows*, moe_mm_grouped*, moe_route_topk_backward. */
 #define MOE_ABI_VERSION 7
-#define MOE_ABI_MINOR 1
+#define MOE_ABI_MINOR 2
 #define MOE_MAX_GROUP 16     /* experts per group buffer ([G1] "What": MMQ_GROUP = 16) */
 #define MOE_MAX_E 2048       /* largest expert count the kernels accept */
 #define MOE_MAX_K 64         /* largest routes per token */
@@ -498,6 +499,100 @@ int moe_balance_loss_backward(const void *logits, int dtype, int64_t ld, int T, 
                               const int32_t *counts, int K, const uint8_t *valid,
                               const float *grad_loss, void *grad_logits, int64_t ld_grad,
                               void *stream);
+
+/* ---- Training the experts in 16 bits ---------------------------------------------------------
+ *
+ * The layer over experts in bf16 or fp16, and its gradients, in the maps' terms (moe_build_maps:
+ * row r is route src[r] = t*K + k, and slot[t*K + k] = r):
+ *   forward    moe_mm_grouped (gate/up with SwiGLU, rows gathered through src, z kept),
+ *              moe_mm_grouped (down), moe_combine_rows
+ *   backward   moe_combine_rows_backward, moe_route_topk_backward; down: moe_mm_grouped_wgrad,
+ *              moe_mm_grouped_dgrad through z; gate/up: moe_mm_grouped_wgrad through src,
+ *              moe_mm_grouped_dgrad; moe_combine_rows without weights sums a token's rows.
+ * Sums are in fp32 and in an order that depends on the sizes alone; a result is rounded once, to
+ * its type.  Rows from offsets[E] on (src = -1) are left as they were.  A matrix's rows lie ld
+ * values apart (ld >= its columns; ld is not looked at for a single row).  Outputs may not overlap
+ * inputs but where that is said. */
+
+/* rows[r] = x[src[r] / K] for r < rows, values of `dtype` copied as they are: x [T x H], out
+ * [rows x H].  A row with src[r] outside [0, T*K) is left as it was.  Any H, any address and
+ * stride that fit the type.  rows <= 2^23.  The gradient: moe_combine_rows with topk_w NULL. */
+int moe_dispatch_rows(const void *x, int dtype, int64_t ldx, int T, int H, const int32_t *src,
+                      int K, int rows, void *out, int64_t ldo, void *stream);
+
+/* out[t] = residual[t] + sum_k topk_w[t*K + k] rows[slot[t*K + k]], k ascending: rows [n_rows x H]
+ * of `dtype`, out [T x H] of out_dtype (dtype, or MOE_F32), residual of out's type or NULL; topk_w
+ * NULL: 1.  A slot outside [0, n_rows) adds nothing.  residual may be out itself, with
+ * ldres = ldo.  Addresses as in moe_dispatch_rows.  T <= 2^23. */
+int moe_combine_rows(const void *rows, int dtype, int64_t ldr, int n_rows, const int32_t *slot,
+                     const float *topk_w, int T, int K, int H, const void *residual, int64_t ldres,
+                     void *out, int out_dtype, int64_t ldo, void *stream);
+
+/* Its gradients from grad_out [T x H] of grad_dtype (dtype, or MOE_F32):
+ *   grad_rows[slot[t*K + k]] = topk_w[t*K + k] grad_out[t]      [n_rows x H] of dtype, or NULL
+ *   grad_w[t*K + k] = sum_i grad_out[t, i] rows[slot[t*K + k], i]        fp32 [T*K], or NULL
+ * (rows is looked at for grad_w alone; it may be grad_rows itself then, with ldgr = ldr).  A slot
+ * outside [0, n_rows) gives grad_w 0 and no row; rows that no slot names are left as they were.  Each
+ * row may be named once.  The residual's gradient is grad_out. */
+int moe_combine_rows_backward(const void *grad_out, int grad_dtype, int64_t ldg,
+                              const int32_t *slot, const float *topk_w, int T, int K, int H,
+                              int n_rows, const void *rows, int dtype, int64_t ldr,
+                              void *grad_rows, int64_t ldgr, float *grad_w, void *stream);
+
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 } moe_activation;
+
+/* The grouped product over every expert in one call: for expert e and its rows r = offsets[e] ..
+ * offsets[e+1]-1 (offsets int32 [E+1], non-decreasing from 0),
+ *   y[r, n] = sum_k a[a(r), k] w[e, n, k] + bias[e, n],   a(r) = src ? src[r] / K : r,
+ *   MOE_ACT_NONE:    out[r] = y[r] + residual[r]
+ *   MOE_ACT_SWIGLU:  out[r, n] = silu(y[r, n]) y[r, n_out + n];  z[r] = y[r] (2 n_out values)
+ * dtype MOE_BF16 or MOE_F16: w [E x n_out x k_in] (2 n_out rows for SwiGLU: gate, then up), a
+ * [n_act x k_in], bias (or NULL) and z (or NULL, SwiGLU only).  out [rows x n_out]: dtype, or for
+ * MOE_ACT_NONE MOE_F32; residual (or NULL, MOE_ACT_NONE only) of out's type; it may be out itself,
+ * with ldres = ldo.  src and K as in moe_mxfp4_mm_grouped.  silu is 0 where it is less than
+ * 2^-119 in magnitude.
+ * w, a, bias, residual, z, out 16-byte aligned, strides multiples of 16 bytes (else MOE_EINVAL).
+ * MOE_EUNSUPPORTED: n_out or k_in not a multiple of 8 or from 2^21 on, E > MOE_MAX_E,
+ * K > MOE_MAX_K, an expert's matrix of 2 GiB or more, with src activations of 2 GiB or more, rows
+ * of a or grad 2^21 values or more apart. */
+int moe_mm_grouped(const void *w, int dtype, int n_out, int k_in, const int32_t *offsets, int E,
+                   const void *a, int64_t lda, int n_act, const int32_t *src, int K, int rows,
+                   const void *bias, int activation, const void *residual, int64_t ldres, void *z,
+                   int64_t ldz, void *out, int out_dtype, int64_t ldo, void *stream);
+
+/* The gradient of the rows it read, from grad [rows x n_out] of dtype (w: n_out rows to an expert,
+ * for gate/up 2 F):
+ *   da[r, k] = sum_n grad[r, n] w[e, n, k]
+ *   z NULL:  out = da [rows x k_in], of dtype or MOE_F32
+ *   else the rows were the SwiGLU of z [rows x 2 k_in], and out [rows x 2 k_in] of dtype is z's
+ *   gradient: with s = 1 / (1 + exp(-z_gate)), da z_up s (1 + z_gate (1 - s)) and da z_gate s.
+ *   out may be z itself, with ldo = ldz.
+ * Alignment and limits as in moe_mm_grouped.  (Rows read through src: out holds them one by one;
+ * moe_combine_rows sums them to tokens.) */
+int moe_mm_grouped_dgrad(const void *w, int dtype, int n_out, int k_in, const int32_t *offsets,
+                         int E, const void *grad, int64_t ldg, int rows, const void *z, int64_t ldz,
+                         void *out, int out_dtype, int64_t ldo, void *stream);
+
+/* The gradients of its weights and bias:
+ *   grad_w[e, n, k] = sum over e's rows of grad[r, n] a[a(r), k],   grad_bias[e, n] = sum grad[r, n]
+ * grad [rows x n_out] and a [n_act x k_in] of dtype; grad_w [E x n_out x k_in] and grad_bias
+ * [E x n_out] (or NULL) of out_dtype (dtype, or MOE_F32), 0 for an expert without rows.  ws:
+ * moe_mm_grouped_wgrad_workspace_size(...) bytes, 16-byte aligned (NULL where that is 0).
+ * Alignment and limits as in moe_mm_grouped. */
+size_t moe_mm_grouped_wgrad_workspace_size(int rows, int n_out, int k_in, int E);
+int moe_mm_grouped_wgrad(const void *grad, int dtype, int64_t ldg, int n_out, const void *a,
+                         int64_t lda, int k_in, int n_act, const int32_t *src, int K,
+                         const int32_t *offsets, int E, int rows, void *grad_w, int out_dtype,
+                         void *grad_bias, void *ws, size_t ws_bytes, void *stream);
+
+/* The gradient of moe_route_topk's logits from grad_w [T x K], its weights':
+ *   grad_logits[t, topk_idx[t, k]] = w_k (gw_k - sum_j w_j gw_j), 0 for the other experts,
+ * rows of E values of `dtype`, ld apart, in fp32 and rounded once; accumulate != 0 adds it to what
+ * grad_logits holds (moe_balance_loss_backward's gradient, say).  The gw of a route whose id is
+ * outside [0, E) counts as 0.  T <= 2^23. */
+int moe_route_topk_backward(const int32_t *topk_idx, const float *topk_w, const float *grad_w,
+                            int T, int E, int K, int accumulate, void *grad_logits, int dtype,
+                            int64_t ld, void *stream);
 
 #ifdef __cplusplus
 }

@@ -20,6 +20,7 @@ QUANT_PER_ROW, QUANT_D4 = 1, 2
 EPI_F32, EPI_SWIGLU_Q8_1, EPI_I32_BLOCKDOTS = 0, 1, 2
 F32, BF16, F16 = 0, 1, 2
 MX_F32, MX_BF16, MX_SWIGLU_MXFP4 = 0, 1, 2
+ACT_NONE, ACT_SWIGLU = 0, 1
 MAX_E, MAX_K = 2048, 64
 WS_COUNTS, WS_OFFSETS, WS_SRC, WS_SLOT, WS_ORDER, WS_NACTIVE, WS_Q8X, WS_GROUPS, WS_HQ8, WS_DM, \
     WS_GROUP_STRIDE, WS_STATUS = range(12)
@@ -77,6 +78,15 @@ SIGNATURES = {
     "moe_balance_workspace_size": (SZ, [I, I]),
     "moe_balance_loss": (I, [P, I, L64, I, I, P, I, P, P, P, P, P, SZ, P]),
     "moe_balance_loss_backward": (I, [P, I, L64, I, I, P, I, P, P, P, L64, P]),
+    "moe_dispatch_rows": (I, [P, I, L64, I, I, P, I, I, P, L64, P]),
+    "moe_combine_rows": (I, [P, I, L64, I, P, P, I, I, I, P, L64, P, I, L64, P]),
+    "moe_combine_rows_backward": (I, [P, I, L64, P, P, I, I, I, I, P, I, L64, P, L64, P, P]),
+    "moe_mm_grouped": (I, [P, I, I, I, P, I, P, L64, I, P, I, I, P, I, P, L64, P, L64, P, I, L64,
+                           P]),
+    "moe_mm_grouped_dgrad": (I, [P, I, I, I, P, I, P, L64, I, P, L64, P, I, L64, P]),
+    "moe_mm_grouped_wgrad_workspace_size": (SZ, [I, I, I, I]),
+    "moe_mm_grouped_wgrad": (I, [P, I, L64, I, P, L64, I, I, P, I, P, I, I, P, I, P, P, SZ, P]),
+    "moe_route_topk_backward": (I, [P, P, P, I, I, I, I, P, I, L64, P]),
 }
 
 
@@ -556,3 +566,146 @@ def balance_loss_backward(logits, counts, K, grad_logits, valid=None, grad_loss=
         logits.data_ptr(), dt, _row_stride("logits", logits, dev), T, E, counts.data_ptr(), K,
         _ptr(valid), _ptr(grad_loss), grad_logits.data_ptr(),
         _row_stride("grad_logits", grad_logits, dev), _current_stream(stream, dev)))
+
+
+# ---- training the experts in 16 bits -----------------------------------------------------------
+# As above; matrices whose rows may be apart are checked for their type and shape here, too.
+def _matrix(name: str, t, device: int, dtype, shape) -> int:
+    """The row stride of a matrix of this type and shape."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: {dtype} {tuple(shape)} is wanted, not {t.dtype} "
+                         f"{tuple(t.shape)}")
+    return _row_stride(name, t, device)
+
+
+def _slots(slot, K: int, T: int, device: int) -> None:
+    if slot.numel() != T * K:
+        raise ValueError(f"slot: {T * K} values are wanted, not {slot.numel()}")
+    _want(device, ("slot", slot, _torch.int32, slot.shape))
+
+
+def dispatch_rows(x, src, out, K, stream=None):
+    """out [rows, H]: row r is x's row src[r] / K (src int32 [rows]); rows whose src is outside x are
+    left as they were."""
+    dt, dev = _dtype(x), _on_current(x)
+    (T, H), rows = x.shape, out.shape[0]
+    _want(dev, ("src", src, _torch.int32, (rows,)))
+    ldo = _matrix("out", out, dev, x.dtype, (rows, H))
+    _check("moe_dispatch_rows", lib().moe_dispatch_rows(
+        x.data_ptr(), dt, _row_stride("x", x, dev), T, H, src.data_ptr(), K, rows, out.data_ptr(),
+        ldo, _current_stream(stream, dev)))
+
+
+def combine_rows(rows, slot, topk_w, out, residual=None, stream=None):
+    """out [T, H] (rows' type or float32) = residual + sum over k of topk_w[t, k] rows[slot[t, k]];
+    topk_w float32 [T, K], or None for the plain sum (K is then slot's T * K values' over T)."""
+    dt, dev = _dtype(rows), _on_current(rows)
+    (R, H), T = rows.shape, out.shape[0]
+    K = topk_w.shape[1] if topk_w is not None else slot.numel() // max(T, 1)
+    _slots(slot, K, T, dev)
+    _want(dev, ("topk_w", topk_w, _torch.float32, (T, K)))
+    odt, ldo = _dtype(out), _matrix("out", out, dev, out.dtype, (T, H))
+    ldres = 0 if residual is None else _matrix("residual", residual, dev, out.dtype, (T, H))
+    _check("moe_combine_rows", lib().moe_combine_rows(
+        rows.data_ptr(), dt, _row_stride("rows", rows, dev), R, slot.data_ptr(), _ptr(topk_w), T, K,
+        H, _ptr(residual), ldres, out.data_ptr(), odt, ldo, _current_stream(stream, dev)))
+
+
+def combine_rows_backward(grad_out, slot, topk_w, grad_rows=None, rows=None, grad_w=None,
+                          stream=None):
+    """From grad_out [T, H] (rows' type or float32): grad_rows [n_rows, H], and with rows
+    [n_rows, H], which may be grad_rows itself, grad_w float32 [T, K]."""
+    gdt, dev = _dtype(grad_out), _on_current(grad_out)
+    T, H = grad_out.shape
+    K = topk_w.shape[1] if topk_w is not None else slot.numel() // max(T, 1)
+    _slots(slot, K, T, dev)
+    if (rows is None) != (grad_w is None):
+        raise ValueError("rows and grad_w are given together")
+    like = rows if rows is not None else grad_rows
+    if like is None:
+        raise ValueError("grad_rows or grad_w is wanted")
+    dt, shape = _dtype(like), (like.shape[0], H)
+    ldr = 0 if rows is None else _matrix("rows", rows, dev, like.dtype, shape)
+    ldgr = 0 if grad_rows is None else _matrix("grad_rows", grad_rows, dev, like.dtype, shape)
+    f32 = _torch.float32
+    _want(dev, ("topk_w", topk_w, f32, (T, K)), ("grad_w", grad_w, f32, (T, K)))
+    _check("moe_combine_rows_backward", lib().moe_combine_rows_backward(
+        grad_out.data_ptr(), gdt, _row_stride("grad_out", grad_out, dev), slot.data_ptr(),
+        _ptr(topk_w), T, K, H, shape[0], _ptr(rows), dt, ldr, _ptr(grad_rows), ldgr, _ptr(grad_w),
+        _current_stream(stream, dev)))
+
+
+def mm_grouped(w, offsets, a, out, src=None, K=1, bias=None, swiglu=False, residual=None, z=None,
+               stream=None):
+    """out [rows, N] = a w^T + bias + residual (w's type or float32), or with swiglu [rows, N / 2]
+    the SwiGLU of gate and up, whose values before it go to z [rows, N].  w [E, N, k] bfloat16 or
+    float16; offsets int32 [E + 1]; a [n_act, k]; src int32 [rows] or None; bias [E, N]."""
+    dt, dev = _dtype(w), _on_current(w)
+    (E, N, k), rows, n_act = w.shape, out.shape[0], a.shape[0]
+    if swiglu and N % 2:
+        raise ValueError("gate and up have as many rows each: N is even")
+    n_out = N // 2 if swiglu else N
+    _want(dev, ("w", w, w.dtype, (E, N, k)), ("offsets", offsets, _torch.int32, (E + 1,)),
+          ("src", src, _torch.int32, (rows,)), ("bias", bias, w.dtype, (E, N)))
+    lda = _matrix("a", a, dev, w.dtype, (n_act, k))
+    odt, ldo = _dtype(out), _matrix("out", out, dev, out.dtype, (rows, n_out))
+    ldres = 0 if residual is None else _matrix("residual", residual, dev, out.dtype, (rows, n_out))
+    ldz = 0 if z is None else _matrix("z", z, dev, w.dtype, (rows, N))
+    _check("moe_mm_grouped", lib().moe_mm_grouped(
+        w.data_ptr(), dt, n_out, k, offsets.data_ptr(), E, a.data_ptr(), lda, n_act, _ptr(src), K,
+        rows, _ptr(bias), ACT_SWIGLU if swiglu else ACT_NONE, _ptr(residual), ldres, _ptr(z), ldz,
+        out.data_ptr(), odt, ldo, _current_stream(stream, dev)))
+
+
+def mm_grouped_dgrad(w, offsets, grad, out, z=None, stream=None):
+    """out [rows, k] = grad w (w's type or float32); with z [rows, 2 k], whose SwiGLU the product
+    read, z's gradient [rows, 2 k].  w [E, N, k], grad [rows, N]."""
+    dt, dev = _dtype(w), _on_current(w)
+    (E, N, k), rows = w.shape, grad.shape[0]
+    _want(dev, ("w", w, w.dtype, (E, N, k)), ("offsets", offsets, _torch.int32, (E + 1,)))
+    ldg = _matrix("grad", grad, dev, w.dtype, (rows, N))
+    cols = k if z is None else 2 * k
+    odt, ldo = _dtype(out), _matrix("out", out, dev, out.dtype, (rows, cols))
+    ldz = 0 if z is None else _matrix("z", z, dev, w.dtype, (rows, cols))
+    _check("moe_mm_grouped_dgrad", lib().moe_mm_grouped_dgrad(
+        w.data_ptr(), dt, N, k, offsets.data_ptr(), E, grad.data_ptr(), ldg, rows, _ptr(z), ldz,
+        out.data_ptr(), odt, ldo, _current_stream(stream, dev)))
+
+
+def mm_grouped_wgrad_workspace_size(rows: int, n_out: int, k_in: int, E: int) -> int:
+    return lib().moe_mm_grouped_wgrad_workspace_size(rows, n_out, k_in, E)
+
+
+def mm_grouped_wgrad(grad, offsets, a, grad_w, ws=None, src=None, K=1, grad_bias=None, stream=None):
+    """grad_w [E, N, k] and grad_bias [E, N] (a's type or float32) from grad [rows, N] and a
+    [n_act, k]; ws: at least mm_grouped_wgrad_workspace_size(rows, N, k, E) bytes, None where that
+    is 0."""
+    dt, dev = _dtype(grad), _on_current(grad)
+    (E, N, k), rows, n_act = grad_w.shape, grad.shape[0], a.shape[0]
+    odt = _dtype(grad_w)
+    _want(dev, ("grad_w", grad_w, grad_w.dtype, (E, N, k)),
+          ("offsets", offsets, _torch.int32, (E + 1,)), ("src", src, _torch.int32, (rows,)),
+          ("grad_bias", grad_bias, grad_w.dtype, (E, N)))
+    if ws is not None:
+        _want(dev, ("ws", ws, ws.dtype, ws.shape))
+    ldg = _matrix("grad", grad, dev, grad.dtype, (rows, N))
+    lda = _matrix("a", a, dev, grad.dtype, (n_act, k))
+    _check("moe_mm_grouped_wgrad", lib().moe_mm_grouped_wgrad(
+        grad.data_ptr(), dt, ldg, N, a.data_ptr(), lda, k, n_act, _ptr(src), K, offsets.data_ptr(),
+        E, rows, grad_w.data_ptr(), odt, _ptr(grad_bias), _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _current_stream(stream, dev)))
+
+
+def route_topk_backward(topk_idx, topk_w, grad_w, grad_logits, accumulate=False, stream=None):
+    """grad_logits [T, E] from topk_idx int32, topk_w and grad_w float32 [T, K]; accumulate adds it to
+    what grad_logits holds."""
+    dt, dev = _dtype(grad_logits), _on_current(grad_logits)
+    T, E = grad_logits.shape
+    K = topk_idx.shape[1]
+    f32 = _torch.float32
+    _want(dev, ("topk_idx", topk_idx, _torch.int32, (T, K)), ("topk_w", topk_w, f32, (T, K)),
+          ("grad_w", grad_w, f32, (T, K)))
+    _check("moe_route_topk_backward", lib().moe_route_topk_backward(
+        topk_idx.data_ptr(), topk_w.data_ptr(), grad_w.data_ptr(), T, E, K, int(accumulate),
+        grad_logits.data_ptr(), dt, _row_stride("grad_logits", grad_logits, dev),
+        _current_stream(stream, dev)))

@@ -1,0 +1,104 @@
+// What the grouped products' kernels share: 16-bit types and their matrix instruction, and what is
+// done with four neighbouring results of one row.
+#pragma once
+
+#include "common.hpp"
+#include "train.hpp"
+
+namespace moe {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+template <int DT>
+struct Half {  // kBF16 or kF16
+  typedef typename Elem<DT>::type T;
+  typedef T v4 __attribute__((ext_vector_type(4)));
+  typedef T v8 __attribute__((ext_vector_type(8)));
+};
+
+// D[i, j] += sum_k P[i, k] Q[j, k] over 16 k: lane l holds row l % 32 of P and of Q, k = 8 (l / 32)
+// .. + 7, and of D column j = l % 32, rows i = 8 (q / 4) + 4 (l / 32) + q % 4 in register q.
+template <int DT>
+__device__ __forceinline__ v16f mfma16(const v4i& p, const v4i& q, const v16f& c) {
+  typedef typename Half<DT>::v8 v8;
+  const v8 a = __builtin_bit_cast(v8, p), b = __builtin_bit_cast(v8, q);
+  if constexpr (DT == kBF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+template <int DT>
+__device__ __forceinline__ v4f load4(const void* p, int64_t at) {
+  typedef typename Elem<DT>::type v4 __attribute__((ext_vector_type(4)));
+  const v4 v = *reinterpret_cast<const v4*>(static_cast<const typename Elem<DT>::type*>(p) + at);
+  return (v4f){(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+}
+template <int DT>
+__device__ __forceinline__ void store4(void* p, int64_t at, const v4f& y) {
+  typedef typename Elem<DT>::type T;
+  typedef T v4 __attribute__((ext_vector_type(4)));
+  *reinterpret_cast<v4*>(static_cast<T*>(p) + at) = (v4){(T)y[0], (T)y[1], (T)y[2], (T)y[3]};
+}
+
+// 1 / (1 + e^-g) with the hardware's exponential and reciprocal, 1 ulp each; the roundings of the
+// exponent's argument and of its constant add 1.25 |g| 2^-24.  The result goes into 16 bits.  From
+// g = -87.4 down 1 + e is 2^126 or more, whose reciprocal the hardware takes for 0.
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
+}
+
+// Forward: results i .. i + 3 of row r of expert e (SwiGLU: y its gates, u its ups), rounded once.
+template <int DT, int ODT, bool SWIGLU>
+__device__ __forceinline__ void finish_forward(const MmProblem& p, int e, int64_t r, int i, v4f y,
+                                               v4f u) {
+  if constexpr (SWIGLU) {
+    if (p.bias) {
+      const int64_t b = (int64_t)e * 2 * p.n_out + i;
+      y += load4<DT>(p.bias, b);
+      u += load4<DT>(p.bias, b + p.n_out);
+    }
+    if (p.z) {
+      store4<DT>(p.z, r * p.ldz + i, y);
+      store4<DT>(p.z, r * p.ldz + p.n_out + i, u);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) y[q] = y[q] * sigmoid(y[q]) * u[q];
+  } else {
+    if (p.bias) y += load4<DT>(p.bias, (int64_t)e * p.n_out + i);
+    if (p.residual) y += load4<ODT>(p.residual, r * p.ldres + i);
+  }
+  store4<ODT>(p.out, r * p.ldo + i, y);
+}
+
+// Dgrad: the input's gradients i .. i + 3 of row r, or through h = g s(g) u with s the sigmoid
+//   dg = dh u s(g) (1 + g (1 - s(g))),   du = dh g s(g).
+template <int DT, int ODT, bool SWIGLU>
+__device__ __forceinline__ void finish_dgrad(const MmProblem& p, int64_t r, int i, v4f y) {
+  if constexpr (SWIGLU) {
+    const v4f g = load4<DT>(p.z, r * p.ldz + i), u = load4<DT>(p.z, r * p.ldz + p.k_in + i);
+    v4f dg, du;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float s = sigmoid(g[q]);
+      du[q] = y[q] * g[q] * s;
+      dg[q] = y[q] * u[q] * s * fmaf(g[q], 1.0f - s, 1.0f);
+    }
+    store4<ODT>(p.out, r * p.ldo + i, dg);
+    store4<ODT>(p.out, r * p.ldo + p.k_in + i, du);
+  } else {
+    store4<ODT>(p.out, r * p.ldo + i, y);
+  }
+}
+
+// a's row that row r reads; the nearest one for a src outside.
+__device__ __forceinline__ int act_row(const MmProblem& p, int64_t r) {
+  if (!p.src) return (int)r;
+  const int v = p.src[r];
+  return v < 0 ? 0 : min((int)((uint64_t)v * p.k_mul >> p.k_shift), p.n_act - 1);
+}
+
+}  // namespace moe
