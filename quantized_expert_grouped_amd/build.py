@@ -21,8 +21,8 @@ LIB = os.path.join(PKG, "libmoe_prefill.so")
 
 SOURCES = ["api.cpp", "walk.cpp", "route.hip", "maps.hip", "quantize.hip", "gather.hip",
            "mmq.hip", "combine.hip", "cpu_share.cpp", "mx_api.cpp", "mx_quantize.hip",
-           "mx_mm.hip", "mx_combine.hip", "balance.hip", "train_api.cpp", "rows.hip", "mm.hip",
-           "route_backward.hip"]
+           "mx_mm.hip", "mx_combine.hip", "balance.hip", "train_api.cpp", "rows.hip", "mm_forward.hip",
+           "mm_dgrad.hip", "mm_wgrad.hip", "route_backward.hip"]
 # plain host code (no HIP): built by the host compiler
 HOST_SOURCES = {"cpu_share.cpp"}
 HOST_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-pthread", "-ffp-contract=off", "-fno-fast-math",

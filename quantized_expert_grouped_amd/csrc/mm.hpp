@@ -7,6 +7,8 @@
 
 namespace moe {
 
+constexpr int kMaxExperts = 2048;  // MOE_MAX_E
+
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef int v2i __attribute__((ext_vector_type(2)));
@@ -94,11 +96,20 @@ __device__ __forceinline__ void finish_dgrad(const MmProblem& p, int64_t r, int 
   }
 }
 
-// a's row that row r reads; the nearest one for a src outside.
-__device__ __forceinline__ int act_row(const MmProblem& p, int64_t r) {
-  if (!p.src) return (int)r;
-  const int v = p.src[r];
-  return v < 0 ? 0 : min((int)((uint64_t)v * p.k_mul >> p.k_shift), p.n_act - 1);
+// The row of a that a route reads; the nearest one for a route outside.
+__device__ __forceinline__ int act_row(const MmProblem& p, int route) {
+  return route < 0 ? 0 : min((int)((uint64_t)route * p.k_mul >> p.k_shift), p.n_act - 1);
+}
+
+// The lane's sum of v over the lanes up to it: within rows of 16 lanes, then over the rows.
+__device__ __forceinline__ int lane_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+  return v;
 }
 
 }  // namespace moe

@@ -1,0 +1,21 @@
+// The grouped product of 16-bit rows and weights,
+//   y[r, n] = sum_k a[a(r), k] w[e, n, k] + bias[e, n]
+// with a residual, or with the SwiGLU of gate and up, in its epilogue.
+#include "mm_launch.hpp"
+
+namespace moe {
+
+template <int DT>
+static hipError_t forward(const MmProblem& p, hipStream_t s) {
+  return p.swiglu            ? launch_tiles<kMmForward, DT, DT, true>(p, s)
+         : p.out_dtype == DT ? launch_tiles<kMmForward, DT, DT, false>(p, s)
+                             : launch_tiles<kMmForward, DT, kF32, false>(p, s);
+}
+
+hipError_t launch_mm_forward(const MmProblem& p_, hipStream_t s) {
+  MmProblem p = p_;
+  set_division(p);
+  return p.dtype == kBF16 ? forward<kBF16>(p, s) : forward<kF16>(p, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,536 @@
+// The grouped products' tile kernel: D[i, j] = sum_c P[i, c] Q[j, c] for a tile of BI x BJ results
+// at a time, c in stages of 64.
+//
+// A stage of an operand goes from memory straight into one of two LDS buffers
+// (buffer_load_dwordx4 ... lds).  An operand whose c is contiguous in memory (w and a in the
+// forward, grad in dgrad) lies there as rows of 64 c, 128 bytes; one whose i or j is contiguous (w
+// in dgrad, both in wgrad) as 64 rows of BI or BJ values, and is turned by the LDS read itself
+// (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 values, and each gets a column of 4).  Both are
+// stored with their 16-byte pieces in an order that lets the lanes of a read take different banks.
+// A piece that is not there (past the matrix's edge, the last row, the end of c) has an offset past
+// the buffer descriptor's size, for which the load writes zeros without a fetch.
+//
+// Workgroups stay and walk through the tiles; the next stage's loads, the next tile's among them,
+// are under way while the products of a stage go on.
+#pragma once
+
+#include "mm.hpp"
+
+namespace moe {
+
+namespace tile {
+
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) const void* lds_ptr_t;
+
+constexpr int kC = 64;                    // c's of a stage
+constexpr uint32_t kNone = 0x80000000u;   // an offset with this bit is past the descriptors' size
+__device__ __forceinline__ uint32_t none_if(bool none) { return none ? kNone : 0u; }
+
+// Wavefronts: WI slices of i by WJ of j, each TI x TJ MFMA tiles of 32 x 32; j's tiles are dealt to
+// the WJ in turn, so that few rows still keep all busy.
+template <int WI_, int WJ_, int TI_, int TJ_>
+struct Geo {
+  static constexpr int WI = WI_, WJ = WJ_, TI = TI_, TJ = TJ_;
+  static constexpr int kWaves = WI * WJ, BI = WI * TI * 32, BJ = WJ * TJ * 32;
+  static constexpr int kPL = BI / 8 / kWaves, kQL = BJ / 8 / kWaves;  // loads of a wavefront, 1 KB each
+  static constexpr int kBuf = (BI + BJ) * kC * 2;
+  static constexpr int kPerCu = kWaves >= 8 ? 1 : 2;  // workgroups of a CU
+  static_assert(TI == 2 && BI % (8 * kWaves) == 0 && BJ % (8 * kWaves) == 0 && kWaves % 2 == 0,
+                "whole loads");
+  static_assert((BI & (BI - 1)) == 0 && (BJ & (BJ - 1)) == 0 && kBuf >= kWaves * 8192, "layout");
+};
+
+template <class G>
+struct Lds {
+  alignas(1024) uint8_t buf[2][G::kBuf];  // P's stage, then Q's
+  int32_t offsets[kMaxExperts + 1];
+};
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(lds_ptr_t)p;
+}
+
+// Lane l's 16 bytes at base + off land at lds + 16 l.  As inline assembly, so that the compiler does
+// not wait for it at every LDS read; the kernel waits itself.  The s_nop keeps the distance that a
+// scalar register written by a vector instruction (a readlane) needs before a memory instruction
+// reads it, and m0's.
+__device__ __forceinline__ void dma16(uint64_t base, uint32_t off, uint32_t lds) {
+  const v4i rsrc = {(int)(uint32_t)base, (int)(uint32_t)(base >> 32), (int)kNone, 0x00020000};
+  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               : : "{m0}"(lds), "v"(off), "s"(rsrc) : "memory");
+}
+
+__device__ __forceinline__ void wait_and_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" : : : "memory");
+}
+__device__ __forceinline__ void barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" : : : "memory");
+}
+
+// A copy that the compiler takes for a new value: what is computed from it stays where it is
+// written instead of being kept in registers through the loops around it.
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// Where piece c of a row of 64 c lies among its 8: at c ^ swizzle(row).
+__device__ __forceinline__ int swizzle(int row) {
+  return ((row >> 1) & 3) | (((row ^ (row >> 3)) & 1) << 2);
+}
+
+// A tile's place and its reduction.
+struct Tile {
+  int expert, row0, nrows, i0, j0, nc;
+};
+
+// One operand's stage, B indices wide.  kWide: c is not the contiguous index.
+template <int B, int kLoads, int kWaves, bool kWide>
+struct Operand {
+  uint64_t base;
+  uint32_t off[kLoads];
+  static constexpr int kRow = B * 2;             // bytes of a c row
+  static constexpr int kRows = 1024 / kRow;      // of them in a load
+  static constexpr int kLanes = 64 / kRows;      // lanes of each
+  static_assert(!kWide || (B >= 128 && B <= 512), "rows of four 64-byte chunks, whole in a load");
+
+  // Load l: this lane's index (narrow) or c (wide), and the first c or index of its piece.
+  __device__ static int row(int l, int lane) { return kWide ? l * kRows + lane / kLanes : 8 * l + lane / 8; }
+  __device__ static int first(int l, int lane) {
+    if (kWide) return ((lane % kLanes) ^ ((row(l, lane) & 3) << 2)) * 8;
+    return ((lane & 7) ^ swizzle(row(l, lane))) * 8;
+  }
+  __device__ __forceinline__ void issue(int i, uint32_t lds, int wave) const {
+    const int l = wave + kWaves * i;
+    dma16(base, off[i], lds + 1024 * l);
+  }
+  // The last stage has only `left` c's.
+  __device__ __forceinline__ void mask(int left, int wave, int lane) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int l = wave + kWaves * i;
+      off[i] |= none_if((kWide ? row(l, lane) : first(l, lane)) >= left);
+    }
+  }
+};
+
+// Where a lane reads an operand: TN tiles, kStep index tiles apart.
+template <int B, int TN, int kStep, bool kWide>
+struct Reader {
+  uint32_t at[kWide ? TN : 4];
+  __device__ __forceinline__ void plan(uint32_t lds, int first_tile, int lane) {
+    if constexpr (kWide) {
+      const int l16 = lane & 15;
+#pragma unroll
+      for (int t = 0; t < TN; ++t)
+        at[t] = lds + (8 * (lane >> 5) + (l16 >> 2)) * (B * 2) +
+                (((first_tile + t * kStep) ^ (l16 >> 2)) * 64) + 32 * ((lane >> 4) & 1) +
+                8 * (l16 & 3);
+    } else {
+      const int row = lane & 31;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        at[s] = lds + (first_tile * 32 + row) * (kC * 2) +
+                16 * ((2 * s + (lane >> 5)) ^ swizzle(row));
+    }
+  }
+  // 16 c's of tile t in step s
+  __device__ __forceinline__ v4i read(int t, int s, uint32_t buf) const {
+    typedef __attribute__((address_space(3))) const v4i* pv4i;
+    typedef __attribute__((address_space(3))) v4s* pv4s;
+    if constexpr (kWide) {
+      const uint32_t a = at[t] + buf + 16 * s * (B * 2);
+      const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((pv4s)(uintptr_t)a);
+      const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((pv4s)(uintptr_t)(a + 4 * (B * 2)));
+      const v2i l = __builtin_bit_cast(v2i, lo), h = __builtin_bit_cast(v2i, hi);
+      return (v4i){l[0], l[1], h[0], h[1]};
+    } else {
+      return *(pv4i)(uintptr_t)(at[s] + buf + t * kStep * 32 * kC * 2);
+    }
+  }
+};
+
+template <int OP, int DT, int ODT, bool SWIGLU, class G>
+struct Kernel {
+  static constexpr bool kGates = OP == kMmForward && SWIGLU;
+  static constexpr bool kPWide = OP != kMmForward, kQWide = OP == kMmWgrad;
+  typedef Operand<G::BI, G::kPL, G::kWaves, kPWide> OpP;
+  typedef Operand<G::BJ, G::kQL, G::kWaves, kQWide> OpQ;
+  static constexpr int kFeat = kGates ? G::BI / 2 : G::BI;  // i's of a tile
+
+  const MmProblem& p;
+  Lds<G>& lds;
+  const int lane, wave, wi, wj;
+  uint32_t ni_tiles, nj_tiles;
+  int before, seg;  // fwd, dgrad: row tiles of the experts before this lane's segment of seg
+
+  __device__ Kernel(const MmProblem& p_, Lds<G>& l)
+      : p(p_), lds(l), lane(threadIdx.x & 63),
+        wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), wi(wave % G::WI),
+        wj(wave / G::WI) {}
+
+  __device__ __forceinline__ int ni() const { return OP == kMmForward ? p.n_out : p.k_in; }
+
+  // The tiles there are, in pairs (or, wgrad, triples) of which i's tile is the fastest.
+  __device__ __forceinline__ uint32_t count() {
+    ni_tiles = (uint32_t)(ni() + kFeat - 1) / kFeat;
+    if constexpr (OP == kMmWgrad) {
+      nj_tiles = (uint32_t)(p.n_out + G::BJ - 1) / G::BJ;
+      return (uint32_t)p.E * nj_tiles * ni_tiles;
+    } else {
+      for (int e = threadIdx.x; e <= p.E; e += G::kWaves * 64)
+        lds.offsets[e] = min(p.offsets[e], p.rows);
+      __syncthreads();
+      seg = (p.E + 63) / 64;
+      int mine = 0;
+      for (int i = 0; i < seg; ++i) {
+        const int e = lane * seg + i;
+        if (e < p.E) mine += tiles_of(lds.offsets[e + 1] - lds.offsets[e]);
+      }
+      before = lane_scan(mine);
+      const uint32_t all = (uint32_t)__builtin_amdgcn_readlane(before, 63) * ni_tiles;
+      before -= mine;
+      return all;
+    }
+  }
+  __device__ static int tiles_of(int n) { return (max(n, 0) + G::BJ - 1) / G::BJ; }
+
+  __device__ __forceinline__ Tile find(uint32_t q) const {
+    Tile t;
+    const int qi = (int)(q % ni_tiles);
+    int qr = (int)(q / ni_tiles);
+    t.i0 = qi * kFeat;
+    if constexpr (OP == kMmWgrad) {
+      t.j0 = qr % (int)nj_tiles * G::BJ;
+      t.expert = qr / (int)nj_tiles;
+      t.row0 = min(p.offsets[t.expert], p.rows);
+      t.nc = max(min(p.offsets[t.expert + 1], p.rows) - t.row0, 0);
+      t.nrows = min(p.n_out - t.j0, G::BJ);
+    } else {
+      const int s = __popcll(ballot(before <= qr)) - 1;  // the last segment that is not past it
+      const int e = s * seg + lane;
+      const bool on = lane < seg && e < p.E;
+      const int o = on ? lds.offsets[e] : 0, n = on ? lds.offsets[e + 1] - o : 0;
+      const int mine = on ? tiles_of(n) : 0, incl = lane_scan(mine);
+      qr -= __builtin_amdgcn_readlane(before, s);
+      const int x = __popcll(ballot(incl <= qr));  // lanes all of whose tiles come before
+      const int m = qr - (__builtin_amdgcn_readlane(incl, x) - __builtin_amdgcn_readlane(mine, x));
+      const int rows = __builtin_amdgcn_readlane(n, x), many = __builtin_amdgcn_readlane(mine, x);
+      const int high = ((rows + many - 1) / many + 31) / 32 * 32;  // equally high, to 32 rows
+      t.expert = s * seg + x;
+      t.row0 = __builtin_amdgcn_readlane(o, x) + m * high;
+      t.nrows = min(rows - m * high, high);
+      t.j0 = 0;
+      t.nc = OP == kMmForward ? p.k_in : p.n_out;
+    }
+    return t;
+  }
+
+  // ---- loads ----
+  struct Loads {
+    OpP P;
+    OpQ Q;
+    int left;             // c's from the next stage on
+    int row;              // wgrad with src: the next stage's first row,
+    uint32_t at;          //   and where in a row of a this lane's pieces lie
+    int route[OP == kMmWgrad ? G::kPL : OP == kMmForward ? G::kQL : 1];
+  };
+
+  // The routes that a tile's first loads need, fetched ahead.
+  __device__ __forceinline__ void fetch(Loads& d, const Tile& t) const {
+    if (OP == kMmDgrad || !p.src) return;
+    if constexpr (OP == kMmForward) {
+      const int lane = here(this->lane);
+#pragma unroll
+      for (int i = 0; i < G::kQL; ++i)
+        d.route[i] = p.src[t.row0 + min(OpQ::row(wave + G::kWaves * i, lane), t.nrows - 1)];
+    } else {
+      routes(d, t.row0, t.nc);
+    }
+  }
+  // Those of a stage's rows, of which `left` are there.
+  __device__ __forceinline__ void routes(Loads& d, int row0, int left) const {
+    const int lane = here(this->lane);
+    if constexpr (OP == kMmWgrad)
+#pragma unroll
+      for (int i = 0; i < G::kPL; ++i) {
+        const int c = OpP::row(wave + G::kWaves * i, lane);
+        d.route[i] = c < left ? p.src[row0 + c] : 0;
+      }
+  }
+
+  __device__ __forceinline__ void plan(Loads& d, const Tile& t) const {
+    constexpr int kSize = 2;
+    const int lane = here(this->lane);
+    const uint64_t w = (uint64_t)p.w + (uint64_t)t.expert * (kGates ? 2 : 1) * p.n_out * p.k_in * kSize;
+    const uint64_t a = (uint64_t)p.a, g = (uint64_t)p.grad;
+    d.left = t.nc;
+    if constexpr (OP == kMmForward) {
+      d.P.base = w;
+#pragma unroll
+      for (int i = 0; i < G::kPL; ++i) {
+        const int l = wave + G::kWaves * i, x = OpP::row(l, lane);
+        int f = t.i0 + x, n = f;
+        if constexpr (kGates) {  // a wavefront's two tiles are gates and their ups
+          f = t.i0 + (x >> 6) * 32 + (x & 31);
+          n = f + (x & 32 ? p.n_out : 0);
+        }
+        d.P.off[i] =
+            (uint32_t)(n * p.k_in + OpP::first(l, lane)) * kSize | none_if(f >= p.n_out);
+      }
+    } else {
+      const int64_t ld = OP == kMmDgrad ? p.k_in : p.lda;
+      const bool gathered = OP == kMmWgrad && p.src;
+      d.P.base = OP == kMmDgrad ? w : gathered ? a : a + (uint64_t)(t.row0 * ld * kSize);
+      const int x = t.i0 + OpP::first(wave, lane);  // the same of all of a wavefront's loads
+      d.row = t.row0;
+      d.at = (uint32_t)x * kSize | none_if(x >= p.k_in);
+      if (!gathered)
+#pragma unroll
+        for (int i = 0; i < G::kPL; ++i)
+          d.P.off[i] =
+              d.at + (uint32_t)OpP::row(wave + G::kWaves * i, lane) * (uint32_t)ld * kSize;
+    }
+    if constexpr (OP == kMmWgrad) {
+      d.Q.base = g + (uint64_t)(t.row0 * p.ldg * kSize);
+#pragma unroll
+      for (int i = 0; i < G::kQL; ++i) {
+        const int l = wave + G::kWaves * i, x = OpQ::first(l, lane);
+        const uint32_t c = OpQ::row(l, lane);
+        d.Q.off[i] = (c * (uint32_t)p.ldg + t.j0 + x) * kSize | none_if(x >= t.nrows);
+      }
+    } else {
+      const int64_t ld = OP == kMmForward ? p.lda : p.ldg;
+      const bool gathered = OP == kMmForward && p.src;
+      d.Q.base = (OP == kMmForward ? a : g) + (gathered ? 0 : (uint64_t)(t.row0 * ld * kSize));
+#pragma unroll
+      for (int i = 0; i < G::kQL; ++i) {
+        const int l = wave + G::kWaves * i, x = OpQ::row(l, lane);
+        uint32_t r = x;
+        if constexpr (OP == kMmForward)
+          if (gathered) r = act_row(p, d.route[i]);
+        d.Q.off[i] = (r * (uint32_t)ld + OpQ::first(l, lane)) * kSize | none_if(x >= t.nrows);
+      }
+    }
+    place(d);
+  }
+  // What changes from stage to stage besides the bases: gathered rows, and the last stage's end.
+  __device__ __forceinline__ void place(Loads& d) const {
+    if (OP == kMmWgrad && p.src) {
+#pragma unroll
+      for (int i = 0; i < G::kPL; ++i)
+        d.P.off[i] = d.at + (uint32_t)act_row(p, d.route[i % (sizeof(d.route) / 4)]) *
+                                (uint32_t)p.lda * 2;
+      d.row += kC;
+      routes(d, d.row, d.left - kC);  // the stage after it
+    }
+    if (d.left < kC) {
+      d.P.mask(d.left, wave, here(lane));
+      d.Q.mask(d.left, wave, here(lane));
+    }
+  }
+
+  // Load i of the next stage to the buffer at `at`, P's first.
+  static constexpr int kLoads = G::kPL + G::kQL;
+  __device__ __forceinline__ void issue(const Loads& d, int i, uint32_t at) const {
+    if (i < G::kPL)
+      d.P.issue(i, at, wave);
+    else
+      d.Q.issue(i - G::kPL, at + G::BI * kC * 2, wave);
+  }
+  // To the stage after the next.
+  __device__ __forceinline__ void advance(Loads& d) const {
+    d.left -= kC;
+    if (d.left <= 0) return;
+    if constexpr (OP == kMmForward) {
+      d.P.base += kC * 2;
+      d.Q.base += kC * 2;
+    } else if constexpr (OP == kMmDgrad) {
+      d.P.base += (uint64_t)kC * p.k_in * 2;
+      d.Q.base += kC * 2;
+    } else {
+      d.Q.base += (uint64_t)(kC * p.ldg * 2);
+      if (!p.src) d.P.base += (uint64_t)(kC * p.lda * 2);
+    }
+    place(d);
+  }
+  // ---- results ----
+  // A wavefront's 64 i's by 32 j's (rows j0 .. of the tile) are turned in 8 KB of LDS, so that 16
+  // lanes hold 64 neighbouring i's of a row.
+  __device__ __forceinline__ void finish(const Tile& t, const v16f& a0, const v16f& a1, int j0,
+                                         uint32_t turn) const {
+    typedef __attribute__((address_space(3))) v4f* pv4f;
+    const int lane = here(this->lane);
+    const int l32 = lane & 31, half = lane >> 5;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {  // i's 32 m + 8 g + 4 half + 0..3 of row l32
+        const v16f& y = m ? a1 : a0;
+        const int piece = 8 * m + 2 * g + half;
+        *(pv4f)(uintptr_t)(turn + l32 * 256 + 16 * (piece ^ (l32 & 15))) =
+            (v4f){y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]};
+      }
+    const int rows = min(t.nrows - j0, 32);
+    auto get = [&](int r, int piece) {
+      return *(pv4f)(uintptr_t)(turn + r * 256 + 16 * (piece ^ (r & 15)));
+    };
+    if constexpr (kGates) {
+      const int i = t.i0 + wi * 32 + (lane & 7) * 4;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = 8 * k + lane / 8;
+        const v4f y = get(r, lane & 7), u = get(r, 8 + (lane & 7));
+        if (r < rows && i < p.n_out)
+          finish_forward<DT, ODT, true>(p, t.expert, (int64_t)t.row0 + j0 + r, i, y, u);
+      }
+    } else {
+      const int i = t.i0 + wi * 64 + (lane & 15) * 4;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = 4 * k + lane / 16;
+        const v4f y = get(r, lane & 15);
+        if (r >= rows || i >= ni()) continue;
+        if constexpr (OP == kMmForward)
+          finish_forward<DT, ODT, false>(p, t.expert, (int64_t)t.row0 + j0 + r, i, y, y);
+        else if constexpr (OP == kMmDgrad)
+          finish_dgrad<DT, ODT, SWIGLU>(p, (int64_t)t.row0 + j0 + r, i, y);
+        else
+          store4<ODT>(p.out, ((int64_t)t.expert * p.n_out + t.j0 + j0 + r) * p.k_in + i, y);
+      }
+    }
+  }
+
+  // ---- the walk ----
+  __device__ __forceinline__ void run() {
+    const uint32_t all = count();
+    // Workgroups go to the 8 XCDs in turn.  Each XCD takes an eighth of the tiles, and its
+    // workgroups walk through it side by side.
+    const uint32_t xcd = blockIdx.x & 7, step = gridDim.x >> 3;
+    const uint32_t end = (uint32_t)((uint64_t)all * (xcd + 1) >> 3);
+    uint32_t q = (uint32_t)((uint64_t)all * xcd >> 3) + (blockIdx.x >> 3);
+    if (q >= end) return;
+
+    const uint32_t buf0 = __builtin_amdgcn_readfirstlane(lds_address(lds.buf[0]));
+    Reader<G::BI, G::TI, 1, kPWide> rp;
+    Reader<G::BJ, G::TJ, G::WJ, kQWide> rq;
+    rp.plan(buf0, wi * G::TI, lane);
+    rq.plan(buf0 + G::BI * kC * 2, wj, lane);
+
+    Loads d;
+    Tile t = find(q), next = t;
+    fetch(d, t);
+    plan(d, t);
+    uint32_t buf = 0;  // the buffer of the stage at work, as an offset
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) issue(d, i, buf0);
+    advance(d);
+    wait_and_barrier();
+    for (;;) {
+      const int stages = max((t.nc + kC - 1) / kC, 1);
+      const bool more = q + step < end;
+      if (more)
+        next = find(q + step);
+      else
+        next.nc = 0;  // a tile of nothing: its loads fetch nothing
+      const int row_tiles = (t.nrows + 31) / 32;
+      const int live = row_tiles > wj ? (row_tiles - wj + G::WJ - 1) / G::WJ : 0;
+      auto go = [&](auto N) {
+        constexpr int NL = decltype(N)::value, M = NL > 0 ? NL : 1;
+        if constexpr (NL <= G::TJ) {
+          if (live != NL) return;
+          v16f acc[G::TI][M];
+#pragma unroll
+          for (int i = 0; i < G::TI; ++i)
+#pragma unroll
+            for (int j = 0; j < NL; ++j)
+#pragma unroll
+              for (int x = 0; x < 16; ++x) acc[i][j][x] = 0.0f;
+          struct Ops {
+            v4i p[G::TI], q[M];
+          };
+          auto read = [&](int s, uint32_t b) {
+            Ops o;
+            if constexpr (NL > 0) {
+#pragma unroll
+              for (int i = 0; i < G::TI; ++i) o.p[i] = rp.read(i, s, b);
+#pragma unroll
+              for (int j = 0; j < NL; ++j) o.q[j] = rq.read(j, s, b);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            return o;
+          };
+          // The products of a step; LOAD: the next stage's loads among them, to the buffer `to`.
+          auto products = [&](const Ops& o, auto LOAD, uint32_t to) {
+            constexpr bool kLoad = decltype(LOAD)::value;
+            constexpr int kMany = NL * G::TI;
+            if constexpr (kMany == 0 && kLoad) {
+#pragma unroll
+              for (int l = 0; l < kLoads; ++l) issue(d, l, to);
+            }
+            constexpr int kOver = kMany > 0 ? kMany : 1;
+#pragma unroll
+            for (int m = 0; m < kMany; ++m) {
+              const int i = m % G::TI, j = m / G::TI;
+              acc[i][j] = mfma16<DT>(o.p[i], o.q[j], acc[i][j]);
+              if constexpr (kLoad) {
+#pragma unroll
+                for (int l = m * kLoads / kOver; l < (m + 1) * kLoads / kOver; ++l)
+                  issue(d, l, to);
+                __builtin_amdgcn_sched_barrier(0);
+              }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (kLoad) advance(d);
+          };
+          // A stage's loads go out in the first step of the one before it; its first operands are
+          // read in that one's last step, after the barrier that ends the reads of it.
+          if (stages == 1) fetch(d, next);
+          Ops now = read(0, buf);
+          int left = stages;
+          do {
+            const uint32_t other = buf ^ (uint32_t)G::kBuf;
+            if (left == 1) plan(d, next);
+            Ops then = read(1, buf);
+            products(now, std::true_type(), buf0 + other);
+            now = read(2, buf);
+            products(then, std::false_type(), 0);
+            then = read(3, buf);
+            products(now, std::false_type(), 0);
+            if (left == 2) fetch(d, next);
+            wait_and_barrier();
+            now = read(0, other);
+            products(then, std::false_type(), 0);
+            buf = other;
+          } while (--left > 0);
+          // the results are turned in the buffer that the last stage was in
+#pragma unroll
+          for (int j = 0; j < NL; ++j)
+            finish(t, acc[0][j], acc[1][j], (j * G::WJ + wj) * 32,
+                   buf0 + (buf ^ (uint32_t)G::kBuf) + 8192 * wave);
+        }
+      };
+      go(std::integral_constant<int, 0>{});
+      go(std::integral_constant<int, 1>{});
+      go(std::integral_constant<int, 2>{});
+      go(std::integral_constant<int, 3>{});
+      go(std::integral_constant<int, 4>{});
+      static_assert(G::TJ <= 4, "instances");
+      if (!more) break;
+      barrier();
+      q += step;
+      t = next;
+    }
+    // no load to LDS is under way when the workgroup ends
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+  }
+};
+
+}  // namespace tile
+
+}  // namespace moe

@@ -75,9 +75,17 @@ struct MmProblem {
   int64_t ldo;
   void* bias_out;          // wgrad: [E x n_out] of out's type, or nullptr
   int n_out, k_in, E, n_act, K, rows;
-  uint32_t k_mul, k_shift;  // division by K (set by the launcher)
+  uint32_t k_mul, k_shift;  // division by K (set_division)
 };
-hipError_t launch_mm(const MmProblem& p, void* ws, hipStream_t s);
+// n / K = n * k_mul >> k_shift for n < 2^30, K <= 64: k_mul K - 2^k_shift <= K <= 2^(k_shift - 30)
+inline void set_division(MmProblem& p) {
+  p.k_shift = 30;
+  while (1 << (p.k_shift - 30) < p.K) ++p.k_shift;
+  p.k_mul = (uint32_t)(((uint64_t)1 << p.k_shift) / p.K + 1);
+}
+hipError_t launch_mm_forward(const MmProblem& p, hipStream_t s);
+hipError_t launch_mm_dgrad(const MmProblem& p, hipStream_t s);
+hipError_t launch_mm_wgrad(const MmProblem& p, void* ws, hipStream_t s);
 size_t mm_wgrad_workspace(int rows, int n_out, int k_in, int E);
 
 // ---- the routing weights' gradient ----------------------------------------------------------

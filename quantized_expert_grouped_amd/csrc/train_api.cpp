@@ -31,6 +31,10 @@ int check_mm(int dtype, int out_dtype, int n_out, int k_in, int E, int rows, int
   if (n_out < 1 || k_in < 1 || E < 1 || rows < 1) return MOE_EINVAL;
   if (!half_dtype(dtype) || (out_dtype != dtype && out_dtype != MOE_F32)) return MOE_EUNSUPPORTED;
   if (n_out % 8 != 0 || k_in % 8 != 0 || E > MOE_MAX_E || rows > kMaxRows) return MOE_EUNSUPPORTED;
+  // tiles are numbered in 31 bits
+  const int64_t nt = n_out / 64 + 1, kt = k_in / 64 + 1;
+  if (((int64_t)rows / 128 + E) * (nt > kt ? nt : kt) >= 1LL << 31 || E * nt * kt >= 1LL << 31)
+    return MOE_EUNSUPPORTED;
   if (n_out >= 1 << 21 || k_in >= 1 << 21 || mat_rows * k_in * 2 >= kMaxBytes) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
@@ -120,7 +124,7 @@ int moe_mm_grouped(const void* w, int dtype, int n_out, int k_in, const int32_t*
   p.z = z, p.ldz = rows == 1 ? 2LL * n_out : ldz;
   p.out = out, p.ldo = rows == 1 ? n_out : ldo;
   p.n_out = n_out, p.k_in = k_in, p.E = E, p.n_act = n_act, p.K = src ? K : 1, p.rows = rows;
-  return status_of(launch_mm(p, nullptr, as_stream(stream)));
+  return status_of(launch_mm_forward(p, as_stream(stream)));
 }
 
 int moe_mm_grouped_dgrad(const void* w, int dtype, int n_out, int k_in, const int32_t* offsets,
@@ -142,7 +146,7 @@ int moe_mm_grouped_dgrad(const void* w, int dtype, int n_out, int k_in, const in
   p.z = const_cast<void*>(z), p.ldz = rows == 1 ? cols : ldz;
   p.out = out, p.ldo = rows == 1 ? cols : ldo;
   p.n_out = n_out, p.k_in = k_in, p.E = E, p.n_act = rows, p.K = 1, p.rows = rows;
-  return status_of(launch_mm(p, nullptr, as_stream(stream)));
+  return status_of(launch_mm_dgrad(p, as_stream(stream)));
 }
 
 size_t moe_mm_grouped_wgrad_workspace_size(int rows, int n_out, int k_in, int E) {
@@ -170,7 +174,7 @@ int moe_mm_grouped_wgrad(const void* grad, int dtype, int64_t ldg, int n_out, co
   p.a = a, p.lda = n_act == 1 ? k_in : lda, p.grad = grad, p.ldg = rows == 1 ? n_out : ldg;
   p.src = src, p.offsets = offsets, p.out = grad_w, p.bias_out = grad_bias;
   p.n_out = n_out, p.k_in = k_in, p.E = E, p.n_act = n_act, p.K = src ? K : 1, p.rows = rows;
-  return status_of(launch_mm(p, ws, as_stream(stream)));
+  return status_of(launch_mm_wgrad(p, ws, as_stream(stream)));
 }
 
 int moe_route_topk_backward(const int32_t* topk_idx, const float* topk_w, const float* grad_w,
