@@ -53,46 +53,15 @@ __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
 }
 
-// Forward: results i .. i + 3 of row r of expert e (SwiGLU: y its gates, u its ups), rounded once.
-template <int DT, int ODT, bool SWIGLU>
-__device__ __forceinline__ void finish_forward(const MmProblem& p, int e, int64_t r, int i, v4f y,
-                                               v4f u) {
-  if constexpr (SWIGLU) {
-    if (p.bias) {
-      const int64_t b = (int64_t)e * 2 * p.n_out + i;
-      y += load4<DT>(p.bias, b);
-      u += load4<DT>(p.bias, b + p.n_out);
-    }
-    if (p.z) {
-      store4<DT>(p.z, r * p.ldz + i, y);
-      store4<DT>(p.z, r * p.ldz + p.n_out + i, u);
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) y[q] = y[q] * sigmoid(y[q]) * u[q];
-  } else {
-    if (p.bias) y += load4<DT>(p.bias, (int64_t)e * p.n_out + i);
-    if (p.residual) y += load4<ODT>(p.residual, r * p.ldres + i);
-  }
-  store4<ODT>(p.out, r * p.ldo + i, y);
-}
-
-// Dgrad: the input's gradients i .. i + 3 of row r, or through h = g s(g) u with s the sigmoid
+// dg and du, the gradients of gate and up from that of h = g s(g) u, s the sigmoid:
 //   dg = dh u s(g) (1 + g (1 - s(g))),   du = dh g s(g).
-template <int DT, int ODT, bool SWIGLU>
-__device__ __forceinline__ void finish_dgrad(const MmProblem& p, int64_t r, int i, v4f y) {
-  if constexpr (SWIGLU) {
-    const v4f g = load4<DT>(p.z, r * p.ldz + i), u = load4<DT>(p.z, r * p.ldz + p.k_in + i);
-    v4f dg, du;
+__device__ __forceinline__ void swiglu_gradient(const v4f& dh, const v4f& g, const v4f& u, v4f& dg,
+                                                v4f& du) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float s = sigmoid(g[q]);
-      du[q] = y[q] * g[q] * s;
-      dg[q] = y[q] * u[q] * s * fmaf(g[q], 1.0f - s, 1.0f);
-    }
-    store4<ODT>(p.out, r * p.ldo + i, dg);
-    store4<ODT>(p.out, r * p.ldo + p.k_in + i, du);
-  } else {
-    store4<ODT>(p.out, r * p.ldo + i, y);
+  for (int q = 0; q < 4; ++q) {
+    const float s = sigmoid(g[q]);
+    du[q] = dh[q] * g[q] * s;
+    dg[q] = dh[q] * u[q] * s * fmaf(g[q], 1.0f - s, 1.0f);
   }
 }
 

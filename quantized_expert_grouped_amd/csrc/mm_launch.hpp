@@ -9,9 +9,9 @@ namespace moe {
 
 template <int OP, int DT, int ODT, bool SWIGLU, class G>
 __global__ __launch_bounds__(G::kWaves * 64, 2) void mm_kernel(MmProblem p) {
-  __shared__ tile::Lds<G> lds;
-  tile::Kernel<OP, DT, ODT, SWIGLU, G> k(p, lds);
-  k.run();
+  typedef tile::Kernel<OP, DT, ODT, SWIGLU, G> K;
+  __shared__ typename K::L lds;
+  K(p, lds).run();
 }
 
 constexpr int kCus = 256;  // MI355X

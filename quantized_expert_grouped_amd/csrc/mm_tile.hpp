@@ -10,8 +10,9 @@
 // A piece that is not there (past the matrix's edge, the last row, the end of c) has an offset past
 // the buffer descriptor's size, for which the load writes zeros without a fetch.
 //
-// Workgroups stay and walk through the tiles; the next stage's loads, the next tile's among them,
-// are under way while the products of a stage go on.
+// Workgroups stay and walk through the tiles.  Loads run two stages ahead of the products, over the
+// tiles' ends: a stage's go out into its buffer when the reads of the stage before the last are
+// done.
 #pragma once
 
 #include "mm.hpp"
@@ -41,10 +42,12 @@ struct Geo {
   static_assert((BI & (BI - 1)) == 0 && (BJ & (BJ - 1)) == 0 && kBuf >= kWaves * 8192, "layout");
 };
 
-template <class G>
+// OWN: the wavefronts have 4 KB each of their own to turn their results in; otherwise the experts'
+// offsets are here, and results are turned in a stage's buffer.
+template <class G, bool OWN>
 struct Lds {
   alignas(1024) uint8_t buf[2][G::kBuf];  // P's stage, then Q's
-  int32_t offsets[kMaxExperts + 1];
+  alignas(16) uint8_t more[OWN ? G::kWaves * 4096 : (kMaxExperts + 1) * 4];
 };
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
@@ -56,7 +59,9 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // scalar register written by a vector instruction (a readlane) needs before a memory instruction
 // reads it, and m0's.
 __device__ __forceinline__ void dma16(uint64_t base, uint32_t off, uint32_t lds) {
-  const v4i rsrc = {(int)(uint32_t)base, (int)(uint32_t)(base >> 32), (int)kNone, 0x00020000};
+  const v4i rsrc = {__builtin_amdgcn_readfirstlane((int)(uint32_t)base),
+                    __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32)), (int)kNone,
+                    0x00020000};
   asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                : : "{m0}"(lds), "v"(off), "s"(rsrc) : "memory");
 }
@@ -163,14 +168,20 @@ struct Kernel {
   typedef Operand<G::BJ, G::kQL, G::kWaves, kQWide> OpQ;
   static constexpr int kFeat = kGates ? G::BI / 2 : G::BI;  // i's of a tile
 
+  // wgrad's results need nothing but their rounding, and its tiles can be short: their ends must not
+  // hold up the loads
+  static constexpr bool kOwnTurn = OP == kMmWgrad;
+  typedef Lds<G, kOwnTurn> L;
+
   const MmProblem& p;
-  Lds<G>& lds;
+  L& lds;
+  int32_t* const offsets;
   const int lane, wave, wi, wj;
   uint32_t ni_tiles, nj_tiles;
   int before, seg;  // fwd, dgrad: row tiles of the experts before this lane's segment of seg
 
-  __device__ Kernel(const MmProblem& p_, Lds<G>& l)
-      : p(p_), lds(l), lane(threadIdx.x & 63),
+  __device__ Kernel(const MmProblem& p_, L& l)
+      : p(p_), lds(l), offsets(reinterpret_cast<int32_t*>(l.more)), lane(threadIdx.x & 63),
         wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), wi(wave % G::WI),
         wj(wave / G::WI) {}
 
@@ -184,13 +195,13 @@ struct Kernel {
       return (uint32_t)p.E * nj_tiles * ni_tiles;
     } else {
       for (int e = threadIdx.x; e <= p.E; e += G::kWaves * 64)
-        lds.offsets[e] = min(p.offsets[e], p.rows);
+        offsets[e] = min(p.offsets[e], p.rows);
       __syncthreads();
       seg = (p.E + 63) / 64;
       int mine = 0;
       for (int i = 0; i < seg; ++i) {
         const int e = lane * seg + i;
-        if (e < p.E) mine += tiles_of(lds.offsets[e + 1] - lds.offsets[e]);
+        if (e < p.E) mine += tiles_of(offsets[e + 1] - offsets[e]);
       }
       before = lane_scan(mine);
       const uint32_t all = (uint32_t)__builtin_amdgcn_readlane(before, 63) * ni_tiles;
@@ -208,14 +219,14 @@ struct Kernel {
     if constexpr (OP == kMmWgrad) {
       t.j0 = qr % (int)nj_tiles * G::BJ;
       t.expert = qr / (int)nj_tiles;
-      t.row0 = min(p.offsets[t.expert], p.rows);
-      t.nc = max(min(p.offsets[t.expert + 1], p.rows) - t.row0, 0);
+      t.row0 = min(__builtin_amdgcn_readfirstlane(p.offsets[t.expert]), p.rows);
+      t.nc = max(min(__builtin_amdgcn_readfirstlane(p.offsets[t.expert + 1]), p.rows) - t.row0, 0);
       t.nrows = min(p.n_out - t.j0, G::BJ);
     } else {
       const int s = __popcll(ballot(before <= qr)) - 1;  // the last segment that is not past it
       const int e = s * seg + lane;
       const bool on = lane < seg && e < p.E;
-      const int o = on ? lds.offsets[e] : 0, n = on ? lds.offsets[e + 1] - o : 0;
+      const int o = on ? offsets[e] : 0, n = on ? offsets[e + 1] - o : 0;
       const int mine = on ? tiles_of(n) : 0, incl = lane_scan(mine);
       qr -= __builtin_amdgcn_readlane(before, s);
       const int x = __popcll(ballot(incl <= qr));  // lanes all of whose tiles come before
@@ -241,27 +252,22 @@ struct Kernel {
     int route[OP == kMmWgrad ? G::kPL : OP == kMmForward ? G::kQL : 1];
   };
 
-  // The routes that a tile's first loads need, fetched ahead.
-  __device__ __forceinline__ void fetch(Loads& d, const Tile& t) const {
+  // The routes that the next stage's loads need, fetched a stage ahead: of the tile's next rows, or
+  // of the next tile's first.
+  __device__ __forceinline__ void fetch(Loads& d, const Tile& t, int row0, int left) const {
     if (OP == kMmDgrad || !p.src) return;
+    const int lane = here(this->lane);
     if constexpr (OP == kMmForward) {
-      const int lane = here(this->lane);
 #pragma unroll
       for (int i = 0; i < G::kQL; ++i)
         d.route[i] = p.src[t.row0 + min(OpQ::row(wave + G::kWaves * i, lane), t.nrows - 1)];
     } else {
-      routes(d, t.row0, t.nc);
-    }
-  }
-  // Those of a stage's rows, of which `left` are there.
-  __device__ __forceinline__ void routes(Loads& d, int row0, int left) const {
-    const int lane = here(this->lane);
-    if constexpr (OP == kMmWgrad)
 #pragma unroll
       for (int i = 0; i < G::kPL; ++i) {
         const int c = OpP::row(wave + G::kWaves * i, lane);
         d.route[i] = c < left ? p.src[row0 + c] : 0;
       }
+    }
   }
 
   __device__ __forceinline__ void plan(Loads& d, const Tile& t) const {
@@ -326,8 +332,6 @@ struct Kernel {
       for (int i = 0; i < G::kPL; ++i)
         d.P.off[i] = d.at + (uint32_t)act_row(p, d.route[i % (sizeof(d.route) / 4)]) *
                                 (uint32_t)p.lda * 2;
-      d.row += kC;
-      routes(d, d.row, d.left - kC);  // the stage after it
     }
     if (d.left < kC) {
       d.P.mask(d.left, wave, here(lane));
@@ -343,67 +347,202 @@ struct Kernel {
     else
       d.Q.issue(i - G::kPL, at + G::BI * kC * 2, wave);
   }
-  // To the stage after the next.
-  __device__ __forceinline__ void advance(Loads& d) const {
+  // The tiles that the loads walk through, ahead of the products.
+  struct Walk {
+    uint32_t q, step, end;
+    Tile next;  // where the loads go after the tile that they are in
+  };
+  // From the stage whose loads are out to the next.
+  __device__ __forceinline__ void advance(Loads& d, Walk& k) const {
     d.left -= kC;
-    if (d.left <= 0) return;
-    if constexpr (OP == kMmForward) {
-      d.P.base += kC * 2;
-      d.Q.base += kC * 2;
-    } else if constexpr (OP == kMmDgrad) {
-      d.P.base += (uint64_t)kC * p.k_in * 2;
-      d.Q.base += kC * 2;
+    if (d.left > 0) {
+      if constexpr (OP == kMmForward) {
+        d.P.base += kC * 2;
+        d.Q.base += kC * 2;
+      } else if constexpr (OP == kMmDgrad) {
+        d.P.base += (uint64_t)kC * p.k_in * 2;
+        d.Q.base += kC * 2;
+      } else {
+        d.Q.base += (uint64_t)(kC * p.ldg * 2);
+        if (!p.src) d.P.base += (uint64_t)(kC * p.lda * 2);
+        d.row += kC;
+      }
+      place(d);
     } else {
-      d.Q.base += (uint64_t)(kC * p.ldg * 2);
-      if (!p.src) d.P.base += (uint64_t)(kC * p.lda * 2);
+      plan(d, k.next);
     }
-    place(d);
+    ahead(d, k);
   }
+  // What the next advance needs.
+  __device__ __forceinline__ void ahead(Loads& d, Walk& k) const {
+    if (d.left <= kC) {  // it goes to the next tile
+      k.q += k.step;
+      if (k.q < k.end)
+        k.next = find(k.q);
+      else
+        k.next.nc = 0;  // a tile of nothing: its loads fetch nothing
+      fetch(d, k.next, k.next.row0, k.next.nc);
+    } else if (OP == kMmWgrad) {
+      fetch(d, k.next, d.row + kC, d.left - kC);
+    }
+  }
+
   // ---- results ----
+  typedef __attribute__((address_space(3))) v4f* pv4f;
   // A wavefront's 64 i's by 32 j's (rows j0 .. of the tile) are turned in 8 KB of LDS, so that 16
   // lanes hold 64 neighbouring i's of a row.
   __device__ __forceinline__ void finish(const Tile& t, const v16f& a0, const v16f& a1, int j0,
                                          uint32_t turn) const {
-    typedef __attribute__((address_space(3))) v4f* pv4f;
     const int lane = here(this->lane);
-    const int l32 = lane & 31, half = lane >> 5;
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {  // i's 32 m + 8 g + 4 half + 0..3 of row l32
-        const v16f& y = m ? a1 : a0;
-        const int piece = 8 * m + 2 * g + half;
-        *(pv4f)(uintptr_t)(turn + l32 * 256 + 16 * (piece ^ (l32 & 15))) =
-            (v4f){y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]};
-      }
     const int rows = min(t.nrows - j0, 32);
+    const int64_t row0 = (int64_t)t.row0 + j0;
+    auto put = [&]() {
+      const int l32 = lane & 31, half = lane >> 5;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {  // i's 32 m + 8 g + 4 half + 0..3 of row l32
+          const v16f& y = m ? a1 : a0;
+          const int piece = 8 * m + 2 * g + half;
+          *(pv4f)(uintptr_t)(turn + l32 * 256 + 16 * (piece ^ (l32 & 15))) =
+              (v4f){y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]};
+        }
+    };
     auto get = [&](int r, int piece) {
       return *(pv4f)(uintptr_t)(turn + r * 256 + 16 * (piece ^ (r & 15)));
     };
     if constexpr (kGates) {
       const int i = t.i0 + wi * 32 + (lane & 7) * 4;
+      v4f bg = {}, bu = {};
+      if (p.bias) {
+        const int64_t b = (int64_t)t.expert * 2 * p.n_out + min(i, p.n_out - 4);
+        bg = load4<DT>(p.bias, b);
+        bu = load4<DT>(p.bias, b + p.n_out);
+      }
+      put();
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int r = 8 * k + lane / 8;
-        const v4f y = get(r, lane & 7), u = get(r, 8 + (lane & 7));
-        if (r < rows && i < p.n_out)
-          finish_forward<DT, ODT, true>(p, t.expert, (int64_t)t.row0 + j0 + r, i, y, u);
+        const v4f g = get(r, lane & 7) + bg, u = get(r, 8 + (lane & 7)) + bu;
+        v4f h;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) h[q] = g[q] * sigmoid(g[q]) * u[q];
+        if (r < rows && i < p.n_out) {
+          if (p.z) {
+            const int64_t at = (row0 + r) * p.ldz + i;
+            store4<DT>(p.z, at, g);
+            store4<DT>(p.z, at + p.n_out, u);
+          }
+          store4<ODT>(p.out, (row0 + r) * p.ldo + i, h);
+        }
       }
     } else {
-      const int i = t.i0 + wi * 64 + (lane & 15) * 4;
+      const int i = t.i0 + wi * 64 + (lane & 15) * 4, safe = min(i, ni() - 4);
+      // what is read comes from the nearest place there is, so that all of it is under way at once
+      constexpr bool kZ = OP == kMmDgrad && SWIGLU;
+      v4f x0[8], x1[kZ ? 8 : 1], b = {};
+      auto at = [&](int k) { return row0 + min(4 * k + lane / 16, rows - 1); };
+      if constexpr (kZ) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          x0[k] = load4<DT>(p.z, at(k) * p.ldz + safe);
+          x1[k] = load4<DT>(p.z, at(k) * p.ldz + p.k_in + safe);
+        }
+      } else if (p.residual) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x0[k] = load4<ODT>(p.residual, at(k) * p.ldres + safe);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x0[k] = b;
+      }
+      if (OP == kMmForward && p.bias) b = load4<DT>(p.bias, (int64_t)t.expert * p.n_out + safe);
+      put();
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int r = 4 * k + lane / 16;
         const v4f y = get(r, lane & 15);
-        if (r >= rows || i >= ni()) continue;
-        if constexpr (OP == kMmForward)
-          finish_forward<DT, ODT, false>(p, t.expert, (int64_t)t.row0 + j0 + r, i, y, y);
-        else if constexpr (OP == kMmDgrad)
-          finish_dgrad<DT, ODT, SWIGLU>(p, (int64_t)t.row0 + j0 + r, i, y);
-        else
-          store4<ODT>(p.out, ((int64_t)t.expert * p.n_out + t.j0 + j0 + r) * p.k_in + i, y);
+        const int64_t o = (row0 + r) * p.ldo + i;
+        if constexpr (kZ) {
+          v4f dg, du;
+          swiglu_gradient(y, x0[k], x1[k], dg, du);
+          if (r < rows && i < ni()) {
+            store4<ODT>(p.out, o, dg);
+            store4<ODT>(p.out, o + p.k_in, du);
+          }
+        } else {
+          if (r < rows && i < ni()) store4<ODT>(p.out, o, y + b + x0[k]);
+        }
       }
     }
+  }
+
+  // wgrad: a wavefront's 32 j's (j0 ..) of 64 i's, rounded first if they are to be, through 4 KB.
+  __device__ __forceinline__ void finish_own(const Tile& t, const v16f& a0, const v16f& a1, int j0,
+                                             uint32_t turn) const {
+    typedef typename Half<DT>::v4 v4h;
+    typedef __attribute__((address_space(3))) v4h* pv4h;
+    typedef __attribute__((address_space(3))) v4i* pv4i;
+    const int lane = here(this->lane);
+    const int l32 = lane & 31, half = lane >> 5, rows = min(t.nrows - j0, 32);
+    constexpr int kSize = ODT == kF32 ? 4 : 2;
+    constexpr int kTiles = ODT == kF32 ? 1 : 2;  // of 128 bytes a row
+    uint8_t* const out = static_cast<uint8_t*>(p.out) +
+                         ((int64_t)t.expert * p.n_out + t.j0 + j0) * p.k_in * kSize;
+#pragma unroll
+    for (int m0 = 0; m0 < 2; m0 += kTiles) {
+#pragma unroll
+      for (int m = m0; m < m0 + kTiles; ++m)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const v16f& y = m ? a1 : a0;
+          const v4f v = {y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]};
+          if constexpr (ODT == kF32) {
+            *(pv4f)(uintptr_t)(turn + l32 * 128 + 16 * ((2 * g + half) ^ (l32 & 7))) = v;
+          } else {
+            typedef typename Half<DT>::T T;
+            const v4h h = {(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+            *(pv4h)(uintptr_t)(turn + l32 * 128 + 16 * ((4 * (m - m0) + g) ^ (l32 & 7)) +
+                               8 * half) = h;
+          }
+        }
+      const int i = t.i0 + wi * 64 + m0 * 32 + (lane & 7) * (16 / kSize);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = 8 * k + lane / 8;
+        const v4i v = *(pv4i)(uintptr_t)(turn + r * 128 + 16 * ((lane & 7) ^ (r & 7)));
+        if (r < rows && i < p.k_in)
+          *reinterpret_cast<v4i*>(out + ((int64_t)r * p.k_in + i) * kSize) = v;
+      }
+    }
+  }
+
+  // Bias gradient, in the tiles of the first i's: the sums of Q's columns over c.  A lane sums 4
+  // columns of every kSumRows-th row of a stage.
+  static constexpr int kSumLanes = G::BJ / 4, kSumRows = 64 / kSumLanes * G::kWaves;
+  __device__ __forceinline__ void sum_columns(v4f& sum, uint32_t q) const {
+    typedef __attribute__((address_space(3))) const typename Half<DT>::v4* pv4h;
+    const int c0 = wave * (64 / kSumLanes) + lane / kSumLanes, l = lane % kSumLanes;
+#pragma unroll
+    for (int c = 0; c < kC; c += kSumRows) {  // kSumRows is a multiple of 4
+      const typename Half<DT>::v4 v =
+          *(pv4h)(uintptr_t)(q + (c + c0) * (G::BJ * 2) + (((l >> 3) ^ (c0 & 3)) * 64) + (l & 7) * 8);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sum[x] += (float)v[x];
+    }
+  }
+  __device__ __forceinline__ void finish_sums(const Tile& t, const v4f& sum, uint32_t turn) const {
+    barrier();  // the other wavefronts' results are turned there
+    *(pv4f)(uintptr_t)(turn + ((wave * (64 / kSumLanes) + lane / kSumLanes) * G::BJ +
+                               lane % kSumLanes * 4) * 4) = sum;
+    barrier();
+    if ((int)threadIdx.x * 4 < t.nrows) {
+      v4f y = {};
+#pragma unroll
+      for (int r = 0; r < kSumRows; ++r)
+        y += *(pv4f)(uintptr_t)(turn + (r * G::BJ + threadIdx.x * 4) * 4);
+      store4<ODT>(p.bias_out, (int64_t)t.expert * p.n_out + t.j0 + threadIdx.x * 4, y);
+    }
+    barrier();
   }
 
   // ---- the walk ----
@@ -422,24 +561,28 @@ struct Kernel {
     rp.plan(buf0, wi * G::TI, lane);
     rq.plan(buf0 + G::BI * kC * 2, wj, lane);
 
+    const uint32_t own = buf0 + 2 * G::kBuf;
     Loads d;
-    Tile t = find(q), next = t;
-    fetch(d, t);
+    Walk ahead_of{q, step, end, find(q)};
+    Tile t = ahead_of.next;
+    fetch(d, t, t.row0, t.nc);
     plan(d, t);
+    ahead(d, ahead_of);
     uint32_t buf = 0;  // the buffer of the stage at work, as an offset
+    auto load_all = [&](uint32_t to) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) issue(d, i, buf0);
-    advance(d);
+      for (int i = 0; i < kLoads; ++i) issue(d, i, to);
+    };
+    load_all(buf0);
+    advance(d, ahead_of);
+    load_all(buf0 + G::kBuf);
     wait_and_barrier();
     for (;;) {
       const int stages = max((t.nc + kC - 1) / kC, 1);
-      const bool more = q + step < end;
-      if (more)
-        next = find(q + step);
-      else
-        next.nc = 0;  // a tile of nothing: its loads fetch nothing
       const int row_tiles = (t.nrows + 31) / 32;
       const int live = row_tiles > wj ? (row_tiles - wj + G::WJ - 1) / G::WJ : 0;
+      const bool sums = OP == kMmWgrad && p.bias_out && t.i0 == 0;
+      v4f sum = {};
       auto go = [&](auto N) {
         constexpr int NL = decltype(N)::value, M = NL > 0 ? NL : 1;
         if constexpr (NL <= G::TJ) {
@@ -465,15 +608,11 @@ struct Kernel {
             __builtin_amdgcn_sched_barrier(0);
             return o;
           };
-          // The products of a step; LOAD: the next stage's loads among them, to the buffer `to`.
+          // The products of a step; LOAD: a stage's loads among them, to the buffer `to`.
           auto products = [&](const Ops& o, auto LOAD, uint32_t to) {
             constexpr bool kLoad = decltype(LOAD)::value;
-            constexpr int kMany = NL * G::TI;
-            if constexpr (kMany == 0 && kLoad) {
-#pragma unroll
-              for (int l = 0; l < kLoads; ++l) issue(d, l, to);
-            }
-            constexpr int kOver = kMany > 0 ? kMany : 1;
+            constexpr int kMany = NL * G::TI, kOver = kMany > 0 ? kMany : 1;
+            if constexpr (kMany == 0 && kLoad) load_all(to);
 #pragma unroll
             for (int m = 0; m < kMany; ++m) {
               const int i = m % G::TI, j = m / G::TI;
@@ -486,33 +625,42 @@ struct Kernel {
               }
             }
             __builtin_amdgcn_sched_barrier(0);
-            if constexpr (kLoad) advance(d);
           };
-          // A stage's loads go out in the first step of the one before it; its first operands are
-          // read in that one's last step, after the barrier that ends the reads of it.
-          if (stages == 1) fetch(d, next);
-          Ops now = read(0, buf);
-          int left = stages;
-          do {
+          // A stage's first operands are read in the last step of the one before, after the barrier
+          // that ends the reads of that one, and the loads of the stage after it go out there.
+          Ops now = read(0, buf), then;
+          auto steps = [&](auto LOAD) {
             const uint32_t other = buf ^ (uint32_t)G::kBuf;
-            if (left == 1) plan(d, next);
-            Ops then = read(1, buf);
-            products(now, std::true_type(), buf0 + other);
+            then = read(1, buf);
+            products(now, std::false_type(), 0);
             now = read(2, buf);
             products(then, std::false_type(), 0);
             then = read(3, buf);
+            if constexpr (OP == kMmWgrad)
+              if (sums) sum_columns(sum, buf0 + buf + G::BI * kC * 2);
             products(now, std::false_type(), 0);
-            if (left == 2) fetch(d, next);
             wait_and_barrier();
+            if constexpr (decltype(LOAD)::value) advance(d, ahead_of);
             now = read(0, other);
-            products(then, std::false_type(), 0);
+            products(then, LOAD, buf0 + buf);
             buf = other;
-          } while (--left > 0);
-          // the results are turned in the buffer that the last stage was in
+          };
+          if constexpr (kOwnTurn) {
+            int left = stages;
+            do steps(std::true_type());
+            while (--left > 0);
 #pragma unroll
-          for (int j = 0; j < NL; ++j)
-            finish(t, acc[0][j], acc[1][j], (j * G::WJ + wj) * 32,
-                   buf0 + (buf ^ (uint32_t)G::kBuf) + 8192 * wave);
+            for (int j = 0; j < NL; ++j)
+              finish_own(t, acc[0][j], acc[1][j], (j * G::WJ + wj) * 32, own + 4096 * wave);
+          } else {
+            // the results are turned in the buffer that the last stage was in
+            for (int left = stages; left > 1; --left) steps(std::true_type());
+            steps(std::false_type());
+#pragma unroll
+            for (int j = 0; j < NL; ++j)
+              finish(t, acc[0][j], acc[1][j], (j * G::WJ + wj) * 32,
+                     buf0 + (buf ^ (uint32_t)G::kBuf) + 8192 * wave);
+          }
         }
       };
       go(std::integral_constant<int, 0>{});
@@ -521,10 +669,15 @@ struct Kernel {
       go(std::integral_constant<int, 3>{});
       go(std::integral_constant<int, 4>{});
       static_assert(G::TJ <= 4, "instances");
-      if (!more) break;
-      barrier();
+      if (sums) finish_sums(t, sum, own);
       q += step;
-      t = next;
+      if (q >= end) break;
+      if constexpr (!kOwnTurn) {
+        barrier();
+        advance(d, ahead_of);
+        load_all(buf0 + (buf ^ (uint32_t)G::kBuf));
+      }
+      t = find(q);
     }
     // no load to LDS is under way when the workgroup ends
     asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
