@@ -1,18 +1,18 @@
 // The grouped products' tile kernel: D[i, j] = sum_c P[i, c] Q[j, c] for a tile of BI x BJ results
-// at a time, c in stages of 64.
+// at a time, c in stages of 32.
 //
-// A stage of an operand goes from memory straight into one of two LDS buffers
+// A stage of an operand goes from memory straight into one of four LDS buffers
 // (buffer_load_dwordx4 ... lds).  An operand whose c is contiguous in memory (w and a in the
-// forward, grad in dgrad) lies there as rows of 64 c, 128 bytes; one whose i or j is contiguous (w
-// in dgrad, both in wgrad) as 64 rows of BI or BJ values, and is turned by the LDS read itself
+// forward, grad in dgrad) lies there as rows of 32 c, 64 bytes; one whose i or j is contiguous (w
+// in dgrad, both in wgrad) as 32 rows of BI or BJ values, and is turned by the LDS read itself
 // (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 values, and each gets a column of 4).  Both are
 // stored with their 16-byte pieces in an order that lets the lanes of a read take different banks.
 // A piece that is not there (past the matrix's edge, the last row, the end of c) has an offset past
 // the buffer descriptor's size, for which the load writes zeros without a fetch.
 //
-// Workgroups stay and walk through the tiles.  Loads run two stages ahead of the products, over the
-// tiles' ends: a stage's go out into its buffer when the reads of the stage before the last are
-// done.
+// Workgroups stay and walk through the tiles.  Loads run four stages ahead of the products, over the
+// tiles' ends: a stage's go out into the buffer whose reads have just ended, while those of two
+// others are still on their way.
 #pragma once
 
 #include "mm.hpp"
@@ -21,10 +21,12 @@ namespace moe {
 
 namespace tile {
 
+typedef unsigned v4u __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) const void* lds_ptr_t;
 
-constexpr int kC = 64;                    // c's of a stage
+constexpr int kC = 32;                    // c's of a stage, two steps of the matrix instruction
+constexpr int kBufs = 4;
 constexpr uint32_t kNone = 0x80000000u;   // an offset with this bit is past the descriptors' size
 __device__ __forceinline__ uint32_t none_if(bool none) { return none ? kNone : 0u; }
 
@@ -34,19 +36,18 @@ template <int WI_, int WJ_, int TI_, int TJ_>
 struct Geo {
   static constexpr int WI = WI_, WJ = WJ_, TI = TI_, TJ = TJ_;
   static constexpr int kWaves = WI * WJ, BI = WI * TI * 32, BJ = WJ * TJ * 32;
-  static constexpr int kPL = BI / 8 / kWaves, kQL = BJ / 8 / kWaves;  // loads of a wavefront, 1 KB each
+  static constexpr int kPL = BI / 16 / kWaves, kQL = BJ / 16 / kWaves;  // loads of a wavefront, 1 KB each
   static constexpr int kBuf = (BI + BJ) * kC * 2;
   static constexpr int kPerCu = kWaves >= 8 ? 1 : 2;  // workgroups of a CU
-  static_assert(TI == 2 && BI % (8 * kWaves) == 0 && BJ % (8 * kWaves) == 0 && kWaves % 2 == 0,
-                "whole loads");
-  static_assert((BI & (BI - 1)) == 0 && (BJ & (BJ - 1)) == 0 && kBuf >= kWaves * 8192, "layout");
+  static_assert(TI == 2 && BI % (16 * kWaves) == 0 && BJ % (16 * kWaves) == 0, "whole loads");
+  static_assert((BI & (BI - 1)) == 0 && (BJ & (BJ - 1)) == 0 && kBuf >= kWaves * 4096, "layout");
 };
 
 // OWN: the wavefronts have 4 KB each of their own to turn their results in; otherwise the experts'
 // offsets are here, and results are turned in a stage's buffer.
 template <class G, bool OWN>
 struct Lds {
-  alignas(1024) uint8_t buf[2][G::kBuf];  // P's stage, then Q's
+  alignas(1024) uint8_t buf[kBufs][G::kBuf];  // P's stage, then Q's
   alignas(16) uint8_t more[OWN ? G::kWaves * 4096 : (kMaxExperts + 1) * 4];
 };
 
@@ -66,8 +67,10 @@ __device__ __forceinline__ void dma16(uint64_t base, uint32_t off, uint32_t lds)
                : : "{m0}"(lds), "v"(off), "s"(rsrc) : "memory");
 }
 
+// Waits for all but the last KEEP of the wavefront's accesses to memory, and for its LDS reads.
+template <int KEEP = 0>
 __device__ __forceinline__ void wait_and_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(KEEP) : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" : : : "memory");
 }
@@ -77,6 +80,13 @@ __device__ __forceinline__ void barrier() {
   asm volatile("" : : : "memory");
 }
 
+// Between lanes of one wavefront, whose LDS operations complete in order, nothing has to wait; but
+// the compiler is to keep what was written by other lanes apart from what was there before.
+__device__ __forceinline__ void lanes_fence() {
+  asm volatile("" : : : "memory");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // A copy that the compiler takes for a new value: what is computed from it stays where it is
 // written instead of being kept in registers through the loops around it.
 __device__ __forceinline__ int here(int v) {
@@ -84,9 +94,13 @@ __device__ __forceinline__ int here(int v) {
   return v;
 }
 
-// Where piece c of a row of 64 c lies among its 8: at c ^ swizzle(row).
-__device__ __forceinline__ int swizzle(int row) {
-  return ((row >> 1) & 3) | (((row ^ (row >> 3)) & 1) << 2);
+// Where piece c of a row of 32 c lies among its 4: at c ^ swizzle(row).
+__device__ __forceinline__ int swizzle(int row) { return (row >> 2) & 3; }
+
+// Read by scalar loads, which no wait for vector ones holds up (nor do they wait for stores).
+typedef __attribute__((address_space(4))) const int32_t* scalar_ptr_t;
+__device__ __forceinline__ scalar_ptr_t constant(const int32_t* p) {
+  return (scalar_ptr_t)(uintptr_t)p;
 }
 
 // A tile's place and its reduction.
@@ -105,10 +119,10 @@ struct Operand {
   static_assert(!kWide || (B >= 128 && B <= 512), "rows of four 64-byte chunks, whole in a load");
 
   // Load l: this lane's index (narrow) or c (wide), and the first c or index of its piece.
-  __device__ static int row(int l, int lane) { return kWide ? l * kRows + lane / kLanes : 8 * l + lane / 8; }
+  __device__ static int row(int l, int lane) { return kWide ? l * kRows + lane / kLanes : 16 * l + lane / 4; }
   __device__ static int first(int l, int lane) {
     if (kWide) return ((lane % kLanes) ^ ((row(l, lane) & 3) << 2)) * 8;
-    return ((lane & 7) ^ swizzle(row(l, lane))) * 8;
+    return ((lane & 3) ^ swizzle(row(l, lane))) * 8;
   }
   __device__ __forceinline__ void issue(int i, uint32_t lds, int wave) const {
     const int l = wave + kWaves * i;
@@ -127,7 +141,7 @@ struct Operand {
 // Where a lane reads an operand: TN tiles, kStep index tiles apart.
 template <int B, int TN, int kStep, bool kWide>
 struct Reader {
-  uint32_t at[kWide ? TN : 4];
+  uint32_t at[kWide ? TN : kC / 16];
   __device__ __forceinline__ void plan(uint32_t lds, int first_tile, int lane) {
     if constexpr (kWide) {
       const int l16 = lane & 15;
@@ -139,7 +153,7 @@ struct Reader {
     } else {
       const int row = lane & 31;
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int s = 0; s < kC / 16; ++s)
         at[s] = lds + (first_tile * 32 + row) * (kC * 2) +
                 16 * ((2 * s + (lane >> 5)) ^ swizzle(row));
     }
@@ -166,6 +180,9 @@ struct Kernel {
   static constexpr bool kPWide = OP != kMmForward, kQWide = OP == kMmWgrad;
   typedef Operand<G::BI, G::kPL, G::kWaves, kPWide> OpP;
   typedef Operand<G::BJ, G::kQL, G::kWaves, kQWide> OpQ;
+  // Tiles of j that are walked through together: the workgroups of an XCD, side by side, then share
+  // what they read in a squarer patch (8191 x 4096 x 4096: see the launch)
+  static constexpr uint32_t kGroup = 4;
   static constexpr int kFeat = kGates ? G::BI / 2 : G::BI;  // i's of a tile
 
   // wgrad's results need nothing but their rounding, and its tiles can be short: their ends must not
@@ -177,7 +194,8 @@ struct Kernel {
   L& lds;
   int32_t* const offsets;
   const int lane, wave, wi, wj;
-  uint32_t ni_tiles, nj_tiles;
+  uint32_t ni_tiles, nj_tiles;  // i's tiles, and of all experts j's
+  uint32_t per_expert;          // wgrad: of one expert
   int before, seg;  // fwd, dgrad: row tiles of the experts before this lane's segment of seg
 
   __device__ Kernel(const MmProblem& p_, L& l)
@@ -191,8 +209,9 @@ struct Kernel {
   __device__ __forceinline__ uint32_t count() {
     ni_tiles = (uint32_t)(ni() + kFeat - 1) / kFeat;
     if constexpr (OP == kMmWgrad) {
-      nj_tiles = (uint32_t)(p.n_out + G::BJ - 1) / G::BJ;
-      return (uint32_t)p.E * nj_tiles * ni_tiles;
+      per_expert = (uint32_t)(p.n_out + G::BJ - 1) / G::BJ;
+      nj_tiles = (uint32_t)p.E * per_expert;
+      return nj_tiles * ni_tiles;
     } else {
       for (int e = threadIdx.x; e <= p.E; e += G::kWaves * 64)
         offsets[e] = min(p.offsets[e], p.rows);
@@ -204,23 +223,26 @@ struct Kernel {
         if (e < p.E) mine += tiles_of(offsets[e + 1] - offsets[e]);
       }
       before = lane_scan(mine);
-      const uint32_t all = (uint32_t)__builtin_amdgcn_readlane(before, 63) * ni_tiles;
+      nj_tiles = (uint32_t)__builtin_amdgcn_readlane(before, 63);
       before -= mine;
-      return all;
+      return nj_tiles * ni_tiles;
     }
   }
   __device__ static int tiles_of(int n) { return (max(n, 0) + G::BJ - 1) / G::BJ; }
 
   __device__ __forceinline__ Tile find(uint32_t q) const {
     Tile t;
-    const int qi = (int)(q % ni_tiles);
-    int qr = (int)(q / ni_tiles);
+    // kGroup tiles of j to all of i's, then the next
+    const uint32_t g = q / (ni_tiles * kGroup), in = q - g * (ni_tiles * kGroup);
+    const uint32_t high = min(kGroup, nj_tiles - g * kGroup);
+    const int qi = (int)(in / high);
+    int qr = (int)(g * kGroup + in - qi * high);
     t.i0 = qi * kFeat;
     if constexpr (OP == kMmWgrad) {
-      t.j0 = qr % (int)nj_tiles * G::BJ;
-      t.expert = qr / (int)nj_tiles;
-      t.row0 = min(__builtin_amdgcn_readfirstlane(p.offsets[t.expert]), p.rows);
-      t.nc = max(min(__builtin_amdgcn_readfirstlane(p.offsets[t.expert + 1]), p.rows) - t.row0, 0);
+      t.expert = qr / (int)per_expert;
+      t.j0 = (qr - t.expert * (int)per_expert) * G::BJ;
+      t.row0 = min(constant(p.offsets)[t.expert], p.rows);
+      t.nc = max(min(constant(p.offsets)[t.expert + 1], p.rows) - t.row0, 0);
       t.nrows = min(p.n_out - t.j0, G::BJ);
     } else {
       const int s = __popcll(ballot(before <= qr)) - 1;  // the last segment that is not past it
@@ -249,7 +271,8 @@ struct Kernel {
     int left;             // c's from the next stage on
     int row;              // wgrad with src: the next stage's first row,
     uint32_t at;          //   and where in a row of a this lane's pieces lie
-    int route[OP == kMmWgrad ? G::kPL : OP == kMmForward ? G::kQL : 1];
+    // forward: each lane's row's; wgrad: those of each load's rows, the same in all lanes
+    int route[OP == kMmWgrad ? G::kPL * OpP::kRows : OP == kMmForward ? G::kQL : 1];
   };
 
   // The routes that the next stage's loads need, fetched a stage ahead: of the tile's next rows, or
@@ -263,10 +286,14 @@ struct Kernel {
         d.route[i] = p.src[t.row0 + min(OpQ::row(wave + G::kWaves * i, lane), t.nrows - 1)];
     } else {
 #pragma unroll
-      for (int i = 0; i < G::kPL; ++i) {
-        const int c = OpP::row(wave + G::kWaves * i, lane);
-        d.route[i] = c < left ? p.src[row0 + c] : 0;
-      }
+      for (int i = 0; i < G::kPL; ++i)
+#pragma unroll
+        for (int h = 0; h < OpP::kRows; ++h) {
+          const int c = (wave + G::kWaves * i) * OpP::kRows + h;
+          // (a row past the last is not fetched; its route is one that is there)
+          d.route[i * OpP::kRows + h] =
+              constant(p.src)[min(row0 + min(c, max(left - 1, 0)), p.rows - 1)];
+        }
     }
   }
 
@@ -328,10 +355,20 @@ struct Kernel {
   // What changes from stage to stage besides the bases: gathered rows, and the last stage's end.
   __device__ __forceinline__ void place(Loads& d) const {
     if (OP == kMmWgrad && p.src) {
+      constexpr int kRows = OP == kMmWgrad ? OpP::kRows : 1;
+      const int h = here(lane) / OpP::kLanes;
 #pragma unroll
-      for (int i = 0; i < G::kPL; ++i)
-        d.P.off[i] = d.at + (uint32_t)act_row(p, d.route[i % (sizeof(d.route) / 4)]) *
-                                (uint32_t)p.lda * 2;
+      for (int i = 0; i < G::kPL; ++i) {
+        uint32_t at = 0;
+#pragma unroll
+        for (int x = 0; x < kRows; ++x) {
+          const uint32_t r =
+              (uint32_t)act_row(p, d.route[(i * kRows + x) % (sizeof(d.route) / 4)]) *
+              (uint32_t)p.lda * 2;
+          at = h == x ? r : at;
+        }
+        d.P.off[i] = d.at + at;
+      }
     }
     if (d.left < kC) {
       d.P.mask(d.left, wave, here(lane));
@@ -352,8 +389,21 @@ struct Kernel {
     uint32_t q, step, end;
     Tile next;  // where the loads go after the tile that they are in
   };
+  // Ahead of advance, once each: the next tile, if it goes there, and the routes that it needs.
+  __device__ __forceinline__ void ahead(Loads& d, Walk& k) const {
+    if (d.left <= kC) {
+      k.q += k.step;
+      if (k.q < k.end)
+        k.next = find(k.q);
+      else
+        k.next.nc = 0;  // a tile of nothing: its loads fetch nothing
+      fetch(d, k.next, k.next.row0, k.next.nc);
+    } else if (OP == kMmWgrad) {
+      fetch(d, k.next, d.row + kC, d.left - kC);
+    }
+  }
   // From the stage whose loads are out to the next.
-  __device__ __forceinline__ void advance(Loads& d, Walk& k) const {
+  __device__ __forceinline__ void advance(Loads& d, const Walk& k) const {
     d.left -= kC;
     if (d.left > 0) {
       if constexpr (OP == kMmForward) {
@@ -371,45 +421,32 @@ struct Kernel {
     } else {
       plan(d, k.next);
     }
-    ahead(d, k);
-  }
-  // What the next advance needs.
-  __device__ __forceinline__ void ahead(Loads& d, Walk& k) const {
-    if (d.left <= kC) {  // it goes to the next tile
-      k.q += k.step;
-      if (k.q < k.end)
-        k.next = find(k.q);
-      else
-        k.next.nc = 0;  // a tile of nothing: its loads fetch nothing
-      fetch(d, k.next, k.next.row0, k.next.nc);
-    } else if (OP == kMmWgrad) {
-      fetch(d, k.next, d.row + kC, d.left - kC);
-    }
   }
 
   // ---- results ----
   typedef __attribute__((address_space(3))) v4f* pv4f;
-  // A wavefront's 64 i's by 32 j's (rows j0 .. of the tile) are turned in 8 KB of LDS, so that 16
-  // lanes hold 64 neighbouring i's of a row.
+  // A wavefront's 64 i's by 32 j's (rows j0 .. of the tile) are turned in 4 KB of LDS, 16 rows at a
+  // time, so that 16 lanes hold 64 neighbouring i's of a row.
   __device__ __forceinline__ void finish(const Tile& t, const v16f& a0, const v16f& a1, int j0,
                                          uint32_t turn) const {
     const int lane = here(this->lane);
     const int rows = min(t.nrows - j0, 32);
     const int64_t row0 = (int64_t)t.row0 + j0;
-    auto put = [&]() {
+    auto put = [&](int half_rows) {
       const int l32 = lane & 31, half = lane >> 5;
+      if ((l32 >> 4) != half_rows) return;
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {  // i's 32 m + 8 g + 4 half + 0..3 of row l32
           const v16f& y = m ? a1 : a0;
           const int piece = 8 * m + 2 * g + half;
-          *(pv4f)(uintptr_t)(turn + l32 * 256 + 16 * (piece ^ (l32 & 15))) =
+          *(pv4f)(uintptr_t)(turn + (l32 & 15) * 256 + 16 * (piece ^ (l32 & 15))) =
               (v4f){y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]};
         }
     };
     auto get = [&](int r, int piece) {
-      return *(pv4f)(uintptr_t)(turn + r * 256 + 16 * (piece ^ (r & 15)));
+      return *(pv4f)(uintptr_t)(turn + (r & 15) * 256 + 16 * (piece ^ (r & 15)));
     };
     if constexpr (kGates) {
       const int i = t.i0 + wi * 32 + (lane & 7) * 4;
@@ -419,9 +456,13 @@ struct Kernel {
         bg = load4<DT>(p.bias, b);
         bu = load4<DT>(p.bias, b + p.n_out);
       }
-      put();
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        if (k % 2 == 0) {
+          lanes_fence();
+          put(k / 2);
+          lanes_fence();
+        }
         const int r = 8 * k + lane / 8;
         const v4f g = get(r, lane & 7) + bg, u = get(r, 8 + (lane & 7)) + bu;
         v4f h;
@@ -456,9 +497,13 @@ struct Kernel {
         for (int k = 0; k < 8; ++k) x0[k] = b;
       }
       if (OP == kMmForward && p.bias) b = load4<DT>(p.bias, (int64_t)t.expert * p.n_out + safe);
-      put();
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
+        if (k % 4 == 0) {
+          lanes_fence();
+          put(k / 4);
+          lanes_fence();
+        }
         const int r = 4 * k + lane / 16;
         const v4f y = get(r, lane & 15);
         const int64_t o = (row0 + r) * p.ldo + i;
@@ -486,10 +531,12 @@ struct Kernel {
     const int l32 = lane & 31, half = lane >> 5, rows = min(t.nrows - j0, 32);
     constexpr int kSize = ODT == kF32 ? 4 : 2;
     constexpr int kTiles = ODT == kF32 ? 1 : 2;  // of 128 bytes a row
-    uint8_t* const out = static_cast<uint8_t*>(p.out) +
-                         ((int64_t)t.expert * p.n_out + t.j0 + j0) * p.k_in * kSize;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        static_cast<uint8_t*>(p.out) + ((int64_t)t.expert * p.n_out + t.j0 + j0) * p.k_in * kSize,
+        0, (int)kNone, 0x00020000);
 #pragma unroll
     for (int m0 = 0; m0 < 2; m0 += kTiles) {
+      lanes_fence();
 #pragma unroll
       for (int m = m0; m < m0 + kTiles; ++m)
 #pragma unroll
@@ -505,13 +552,16 @@ struct Kernel {
                                8 * half) = h;
           }
         }
+      lanes_fence();
       const int i = t.i0 + wi * 64 + m0 * 32 + (lane & 7) * (16 / kSize);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int r = 8 * k + lane / 8;
         const v4i v = *(pv4i)(uintptr_t)(turn + r * 128 + 16 * ((lane & 7) ^ (r & 7)));
-        if (r < rows && i < p.k_in)
-          *reinterpret_cast<v4i*>(out + ((int64_t)r * p.k_in + i) * kSize) = v;
+        // past the edges the offset is past the descriptor: each wavefront issues the same stores
+        __builtin_amdgcn_raw_buffer_store_b128(
+            __builtin_bit_cast(v4u, v), rsrc,
+            ((r * p.k_in + i) * kSize) | none_if(r >= rows || i >= p.k_in), 0, 0);
       }
     }
   }
@@ -561,22 +611,29 @@ struct Kernel {
     rp.plan(buf0, wi * G::TI, lane);
     rq.plan(buf0 + G::BI * kC * 2, wj, lane);
 
-    const uint32_t own = buf0 + 2 * G::kBuf;
+    const uint32_t own = buf0 + kBufs * G::kBuf;
     Loads d;
-    Walk ahead_of{q, step, end, find(q)};
-    Tile t = ahead_of.next;
-    fetch(d, t, t.row0, t.nc);
-    plan(d, t);
-    ahead(d, ahead_of);
-    uint32_t buf = 0;  // the buffer of the stage at work, as an offset
+    Walk walk{q, step, end, find(q)};
+    Tile t = walk.next;
     auto load_all = [&](uint32_t to) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) issue(d, i, to);
     };
+    fetch(d, t, t.row0, t.nc);
+    plan(d, t);
     load_all(buf0);
-    advance(d, ahead_of);
-    load_all(buf0 + G::kBuf);
-    wait_and_barrier();
+    for (int s = 1; s < kBufs; ++s) {
+      ahead(d, walk);
+      advance(d, walk);
+      load_all(buf0 + s * G::kBuf);
+    }
+    // Stage s + 1 has landed when no more than the loads of two stages, which followed it, are out.
+    constexpr int kKeep = 2 * kLoads;
+    wait_and_barrier<kKeep + kLoads>();
+    uint32_t buf = 0;  // the buffer of the stage at work, as an offset
+    // Own turn: three more waits come before the loads that followed a tile's stores.
+    constexpr int kStores = G::TJ * (ODT == kF32 ? 8 : 4);
+    int relaxed = 0;
     for (;;) {
       const int stages = max((t.nc + kC - 1) / kC, 1);
       const int row_tiles = (t.nrows + 31) / 32;
@@ -608,58 +665,73 @@ struct Kernel {
             __builtin_amdgcn_sched_barrier(0);
             return o;
           };
-          // The products of a step; LOAD: a stage's loads among them, to the buffer `to`.
-          auto products = [&](const Ops& o, auto LOAD, uint32_t to) {
-            constexpr bool kLoad = decltype(LOAD)::value;
-            constexpr int kMany = NL * G::TI, kOver = kMany > 0 ? kMany : 1;
-            if constexpr (kMany == 0 && kLoad) load_all(to);
+          // The products of a step, with `first` after the first of them and a part of `loads` after
+          // each.
+          auto products = [&](const Ops& o, auto first, auto loads) {
+            constexpr int kMany = NL * G::TI;
+            if constexpr (kMany == 0) {
+              first();
+              loads(0, 1);
+            }
 #pragma unroll
             for (int m = 0; m < kMany; ++m) {
               const int i = m % G::TI, j = m / G::TI;
               acc[i][j] = mfma16<DT>(o.p[i], o.q[j], acc[i][j]);
-              if constexpr (kLoad) {
-#pragma unroll
-                for (int l = m * kLoads / kOver; l < (m + 1) * kLoads / kOver; ++l)
-                  issue(d, l, to);
-                __builtin_amdgcn_sched_barrier(0);
-              }
+              if (m == 0) first();
+              loads(m, kMany);
             }
             __builtin_amdgcn_sched_barrier(0);
           };
-          // A stage's first operands are read in the last step of the one before, after the barrier
-          // that ends the reads of that one, and the loads of the stage after it go out there.
-          Ops now = read(0, buf), then;
-          auto steps = [&](auto LOAD) {
-            const uint32_t other = buf ^ (uint32_t)G::kBuf;
-            then = read(1, buf);
-            products(now, std::false_type(), 0);
-            now = read(2, buf);
-            products(then, std::false_type(), 0);
-            then = read(3, buf);
+          auto nothing = []() {};
+          auto no_loads = [](int, int) {};
+          Ops now = read(0, buf);
+          // A stage's first operands are read in the second step of the one before, after the
+          // barrier that ends the reads of that one; then its buffer is loaded again.
+          auto stage = [&](auto LOAD) {
+            const uint32_t other = (buf + G::kBuf) % (kBufs * G::kBuf);
+            const Ops then = read(1, buf);
             if constexpr (OP == kMmWgrad)
               if (sums) sum_columns(sum, buf0 + buf + G::BI * kC * 2);
-            products(now, std::false_type(), 0);
-            wait_and_barrier();
-            if constexpr (decltype(LOAD)::value) advance(d, ahead_of);
+            products(now, [&]() {
+              __builtin_amdgcn_sched_barrier(0);
+              ahead(d, walk);
+            }, no_loads);
+            if (kOwnTurn && relaxed > 0) {
+              wait_and_barrier<kKeep + kStores>();
+              --relaxed;
+            } else {
+              wait_and_barrier<kKeep>();
+            }
             now = read(0, other);
-            products(then, LOAD, buf0 + buf);
+            if constexpr (decltype(LOAD)::value) {
+              advance(d, walk);
+              products(then, nothing, [&](int m, int many) {
+#pragma unroll
+                for (int l = m * kLoads / many; l < (m + 1) * kLoads / many; ++l)
+                  issue(d, l, buf0 + buf);
+                __builtin_amdgcn_sched_barrier(0);
+              });
+            } else {
+              products(then, nothing, no_loads);
+            }
             buf = other;
           };
           if constexpr (kOwnTurn) {
             int left = stages;
-            do steps(std::true_type());
+            do stage(std::true_type());
             while (--left > 0);
 #pragma unroll
             for (int j = 0; j < NL; ++j)
               finish_own(t, acc[0][j], acc[1][j], (j * G::WJ + wj) * 32, own + 4096 * wave);
+            relaxed = NL == G::TJ ? 3 : 0;
           } else {
             // the results are turned in the buffer that the last stage was in
-            for (int left = stages; left > 1; --left) steps(std::true_type());
-            steps(std::false_type());
+            for (int left = stages; left > 1; --left) stage(std::true_type());
+            const uint32_t turn = buf0 + buf + 4096 * wave;
+            stage(std::false_type());
 #pragma unroll
             for (int j = 0; j < NL; ++j)
-              finish(t, acc[0][j], acc[1][j], (j * G::WJ + wj) * 32,
-                     buf0 + (buf ^ (uint32_t)G::kBuf) + 8192 * wave);
+              finish(t, acc[0][j], acc[1][j], (j * G::WJ + wj) * 32, turn);
           }
         }
       };
@@ -674,8 +746,8 @@ struct Kernel {
       if (q >= end) break;
       if constexpr (!kOwnTurn) {
         barrier();
-        advance(d, ahead_of);
-        load_all(buf0 + (buf ^ (uint32_t)G::kBuf));
+        advance(d, walk);
+        load_all(buf0 + (buf + (kBufs - 1) * G::kBuf) % (kBufs * G::kBuf));
       }
       t = find(q);
     }
