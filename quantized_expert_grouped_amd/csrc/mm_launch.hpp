@@ -32,13 +32,19 @@ hipError_t launch_geo(const MmProblem& p, hipStream_t s) {
   mm_kernel<OP, DT, ODT, SWIGLU, G><<<grid, G::kWaves * 64, 0, s>>>(p);
   return hipGetLastError();
 }
-typedef tile::Geo<4, 2, 2, 4> Large;  // 256 x 256
-typedef tile::Geo<2, 2, 2, 2> Small;  // 128 x 128, two workgroups a CU
+// 256 x 256, and 128 x 128 with two workgroups a CU.  In stages of 64 a narrow operand's rows come in
+// whole 128-byte lines; wgrad has none, and its short tiles like more loads on their way.
+template <int OP>
+using Large = tile::Geo<4, 2, 2, 4, OP == kMmWgrad ? 32 : 64>;
+template <int OP>
+using Small = tile::Geo<2, 2, 2, 2, OP == kMmWgrad ? 32 : 64>;
 
 template <int OP, int DT, int ODT, bool SWIGLU>
 hipError_t launch_tiles(const MmProblem& p, hipStream_t s) {
-  return most_tiles<Large>(p) >= kCus ? launch_geo<OP, DT, ODT, SWIGLU, Large>(p, s)
-                                      : launch_geo<OP, DT, ODT, SWIGLU, Small>(p, s);
+  const bool few_rows = OP != kMmWgrad && p.rows / p.E <= 64;
+  return most_tiles<Large<OP>>(p) >= kCus && !few_rows
+             ? launch_geo<OP, DT, ODT, SWIGLU, Large<OP>>(p, s)
+             : launch_geo<OP, DT, ODT, SWIGLU, Small<OP>>(p, s);
 }
 
 }  // namespace moe

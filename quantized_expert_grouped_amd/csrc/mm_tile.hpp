@@ -1,18 +1,18 @@
 // The grouped products' tile kernel: D[i, j] = sum_c P[i, c] Q[j, c] for a tile of BI x BJ results
-// at a time, c in stages of 32.
+// at a time, c in stages of 32 or 64.
 //
-// A stage of an operand goes from memory straight into one of four LDS buffers
+// A stage of an operand goes from memory straight into one of four or two LDS buffers
 // (buffer_load_dwordx4 ... lds).  An operand whose c is contiguous in memory (w and a in the
-// forward, grad in dgrad) lies there as rows of 32 c, 64 bytes; one whose i or j is contiguous (w
-// in dgrad, both in wgrad) as 32 rows of BI or BJ values, and is turned by the LDS read itself
+// forward, grad in dgrad) lies there as rows of a stage's c; one whose i or j is contiguous (w
+// in dgrad, both in wgrad) as a stage's rows of BI or BJ values, and is turned by the LDS read itself
 // (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 values, and each gets a column of 4).  Both are
 // stored with their 16-byte pieces in an order that lets the lanes of a read take different banks.
 // A piece that is not there (past the matrix's edge, the last row, the end of c) has an offset past
 // the buffer descriptor's size, for which the load writes zeros without a fetch.
 //
-// Workgroups stay and walk through the tiles.  Loads run four stages ahead of the products, over the
-// tiles' ends: a stage's go out into the buffer whose reads have just ended, while those of two
-// others are still on their way.
+// Workgroups stay and walk through the tiles.  Loads run as many stages ahead of the products as
+// there are buffers, over the tiles' ends: a stage's go out into the buffer whose reads have just
+// ended, while with four those of two others are still on their way.
 #pragma once
 
 #include "mm.hpp"
@@ -25,21 +25,23 @@ typedef unsigned v4u __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) const void* lds_ptr_t;
 
-constexpr int kC = 32;                    // c's of a stage, two steps of the matrix instruction
-constexpr int kBufs = 4;
 constexpr uint32_t kNone = 0x80000000u;   // an offset with this bit is past the descriptors' size
 __device__ __forceinline__ uint32_t none_if(bool none) { return none ? kNone : 0u; }
 
 // Wavefronts: WI slices of i by WJ of j, each TI x TJ MFMA tiles of 32 x 32; j's tiles are dealt to
-// the WJ in turn, so that few rows still keep all busy.
-template <int WI_, int WJ_, int TI_, int TJ_>
+// the WJ in turn, so that few rows still keep all busy.  C c's make a stage, a step of the matrix
+// instruction 16 of them.
+template <int WI_, int WJ_, int TI_, int TJ_, int C_>
 struct Geo {
-  static constexpr int WI = WI_, WJ = WJ_, TI = TI_, TJ = TJ_;
+  static constexpr int WI = WI_, WJ = WJ_, TI = TI_, TJ = TJ_, kC = C_, kBufs = 128 / C_;
+  static constexpr int kSteps = kC / 16, kPieces = kC / 8;  // of a narrow row
   static constexpr int kWaves = WI * WJ, BI = WI * TI * 32, BJ = WJ * TJ * 32;
-  static constexpr int kPL = BI / 16 / kWaves, kQL = BJ / 16 / kWaves;  // loads of a wavefront, 1 KB each
+  static constexpr int kPL = BI * kC / 512 / kWaves, kQL = BJ * kC / 512 / kWaves;  // loads of 1 KB
   static constexpr int kBuf = (BI + BJ) * kC * 2;
   static constexpr int kPerCu = kWaves >= 8 ? 1 : 2;  // workgroups of a CU
-  static_assert(TI == 2 && BI % (16 * kWaves) == 0 && BJ % (16 * kWaves) == 0, "whole loads");
+  static_assert(TI == 2 && BI * kC % (512 * kWaves) == 0 && BJ * kC % (512 * kWaves) == 0 &&
+                    (kC == 32 || kC == 64),
+                "whole loads");
   static_assert((BI & (BI - 1)) == 0 && (BJ & (BJ - 1)) == 0 && kBuf >= kWaves * 4096, "layout");
 };
 
@@ -47,7 +49,7 @@ struct Geo {
 // offsets are here, and results are turned in a stage's buffer.
 template <class G, bool OWN>
 struct Lds {
-  alignas(1024) uint8_t buf[kBufs][G::kBuf];  // P's stage, then Q's
+  alignas(1024) uint8_t buf[G::kBufs][G::kBuf];  // P's stage, then Q's
   alignas(16) uint8_t more[OWN ? G::kWaves * 4096 : (kMaxExperts + 1) * 4];
 };
 
@@ -94,8 +96,12 @@ __device__ __forceinline__ int here(int v) {
   return v;
 }
 
-// Where piece c of a row of 32 c lies among its 4: at c ^ swizzle(row).
-__device__ __forceinline__ int swizzle(int row) { return (row >> 2) & 3; }
+// Where piece c of a narrow row lies among its 4 or 8: at c ^ swizzle(row).
+template <int C>
+__device__ __forceinline__ int swizzle(int row) {
+  if (C == 32) return (row >> 2) & 3;
+  return ((row >> 1) & 3) | (((row ^ (row >> 3)) & 1) << 2);
+}
 
 // Read by scalar loads, which no wait for vector ones holds up (nor do they wait for stores).
 typedef __attribute__((address_space(4))) const int32_t* scalar_ptr_t;
@@ -108,8 +114,8 @@ struct Tile {
   int expert, row0, nrows, i0, j0, nc;
 };
 
-// One operand's stage, B indices wide.  kWide: c is not the contiguous index.
-template <int B, int kLoads, int kWaves, bool kWide>
+// One operand's stage of C c's, B indices wide.  kWide: c is not the contiguous index.
+template <int B, int C, int kLoads, int kWaves, bool kWide>
 struct Operand {
   uint64_t base;
   uint32_t off[kLoads];
@@ -119,10 +125,12 @@ struct Operand {
   static_assert(!kWide || (B >= 128 && B <= 512), "rows of four 64-byte chunks, whole in a load");
 
   // Load l: this lane's index (narrow) or c (wide), and the first c or index of its piece.
-  __device__ static int row(int l, int lane) { return kWide ? l * kRows + lane / kLanes : 16 * l + lane / 4; }
+  __device__ static int row(int l, int lane) { 
+    return kWide ? l * kRows + lane / kLanes : 512 / C * l + lane / (C / 8);
+  }
   __device__ static int first(int l, int lane) {
     if (kWide) return ((lane % kLanes) ^ ((row(l, lane) & 3) << 2)) * 8;
-    return ((lane & 3) ^ swizzle(row(l, lane))) * 8;
+    return (lane % (C / 8) ^ swizzle<C>(row(l, lane))) * 8;
   }
   __device__ __forceinline__ void issue(int i, uint32_t lds, int wave) const {
     const int l = wave + kWaves * i;
@@ -139,9 +147,9 @@ struct Operand {
 };
 
 // Where a lane reads an operand: TN tiles, kStep index tiles apart.
-template <int B, int TN, int kStep, bool kWide>
+template <int B, int C, int TN, int kStep, bool kWide>
 struct Reader {
-  uint32_t at[kWide ? TN : kC / 16];
+  uint32_t at[kWide ? TN : C / 16];
   __device__ __forceinline__ void plan(uint32_t lds, int first_tile, int lane) {
     if constexpr (kWide) {
       const int l16 = lane & 15;
@@ -153,9 +161,9 @@ struct Reader {
     } else {
       const int row = lane & 31;
 #pragma unroll
-      for (int s = 0; s < kC / 16; ++s)
-        at[s] = lds + (first_tile * 32 + row) * (kC * 2) +
-                16 * ((2 * s + (lane >> 5)) ^ swizzle(row));
+      for (int s = 0; s < C / 16; ++s)
+        at[s] = lds + (first_tile * 32 + row) * (C * 2) +
+                16 * ((2 * s + (lane >> 5)) ^ swizzle<C>(row));
     }
   }
   // 16 c's of tile t in step s
@@ -169,7 +177,7 @@ struct Reader {
       const v2i l = __builtin_bit_cast(v2i, lo), h = __builtin_bit_cast(v2i, hi);
       return (v4i){l[0], l[1], h[0], h[1]};
     } else {
-      return *(pv4i)(uintptr_t)(at[s] + buf + t * kStep * 32 * kC * 2);
+      return *(pv4i)(uintptr_t)(at[s] + buf + t * kStep * 32 * C * 2);
     }
   }
 };
@@ -178,8 +186,9 @@ template <int OP, int DT, int ODT, bool SWIGLU, class G>
 struct Kernel {
   static constexpr bool kGates = OP == kMmForward && SWIGLU;
   static constexpr bool kPWide = OP != kMmForward, kQWide = OP == kMmWgrad;
-  typedef Operand<G::BI, G::kPL, G::kWaves, kPWide> OpP;
-  typedef Operand<G::BJ, G::kQL, G::kWaves, kQWide> OpQ;
+  static constexpr int kC = G::kC, kBufs = G::kBufs;
+  typedef Operand<G::BI, kC, G::kPL, G::kWaves, kPWide> OpP;
+  typedef Operand<G::BJ, kC, G::kQL, G::kWaves, kQWide> OpQ;
   // Tiles of j that are walked through together: the workgroups of an XCD, side by side, then share
   // what they read in a squarer patch (8191 x 4096 x 4096: see the launch)
   static constexpr uint32_t kGroup = 4;
@@ -389,21 +398,8 @@ struct Kernel {
     uint32_t q, step, end;
     Tile next;  // where the loads go after the tile that they are in
   };
-  // Ahead of advance, once each: the next tile, if it goes there, and the routes that it needs.
-  __device__ __forceinline__ void ahead(Loads& d, Walk& k) const {
-    if (d.left <= kC) {
-      k.q += k.step;
-      if (k.q < k.end)
-        k.next = find(k.q);
-      else
-        k.next.nc = 0;  // a tile of nothing: its loads fetch nothing
-      fetch(d, k.next, k.next.row0, k.next.nc);
-    } else if (OP == kMmWgrad) {
-      fetch(d, k.next, d.row + kC, d.left - kC);
-    }
-  }
-  // From the stage whose loads are out to the next.
-  __device__ __forceinline__ void advance(Loads& d, const Walk& k) const {
+  // From the stage whose loads are out to the next; what the one after it needs is fetched.
+  __device__ __forceinline__ void advance(Loads& d, Walk& k) const {
     d.left -= kC;
     if (d.left > 0) {
       if constexpr (OP == kMmForward) {
@@ -421,50 +417,101 @@ struct Kernel {
     } else {
       plan(d, k.next);
     }
+    ahead(d, k);
+  }
+  __device__ __forceinline__ void ahead(Loads& d, Walk& k) const {
+    if (d.left <= kC) {  // the next stage is another tile's
+      k.q += k.step;
+      if (k.q < k.end)
+        k.next = find(k.q);
+      else
+        k.next.nc = 0;  // a tile of nothing: its loads fetch nothing
+      fetch(d, k.next, k.next.row0, k.next.nc);
+    } else if (OP == kMmWgrad) {
+      fetch(d, k.next, d.row + kC, d.left - kC);
+    }
   }
 
   // ---- results ----
   typedef __attribute__((address_space(3))) v4f* pv4f;
-  // A wavefront's 64 i's by 32 j's (rows j0 .. of the tile) are turned in 4 KB of LDS, 16 rows at a
-  // time, so that 16 lanes hold 64 neighbouring i's of a row.
+  // What the results of a wavefront's 64 i's by 32 j's (rows j0 .. of the tile) are joined with: the
+  // residual, or gate and up.  All is read at once, from the nearest place there is.
+  static constexpr bool kZ = OP == kMmDgrad && SWIGLU;
+  static constexpr bool kResidual = OP == kMmForward && !SWIGLU;
+  static constexpr int XDT = kZ ? DT : ODT;
+  typedef typename Elem<XDT>::type X4 __attribute__((ext_vector_type(4)));
+  struct Extra {
+    X4 a[kZ || kResidual ? 8 : 1], b[kZ ? 8 : 1];
+  };
+  __device__ __forceinline__ void read_extra(Extra& x, const Tile& t, int j0) const {
+    const int lane = here(this->lane);
+    const int rows = max(min(t.nrows - j0, 32), 1);
+    const int i = min(t.i0 + wi * 64 + (lane & 15) * 4, ni() - 4);
+    const int64_t row0 = (int64_t)t.row0 + min(j0, t.nrows - 1);
+    const typename Elem<XDT>::type* from =
+        static_cast<const typename Elem<XDT>::type*>(kZ ? p.z : p.residual);
+    const int64_t ld = kZ ? p.ldz : p.ldres;
+    if (!kZ && !(kResidual && p.residual)) return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t at = (row0 + min(4 * k + lane / 16, rows - 1)) * ld + i;
+      x.a[kZ || kResidual ? k : 0] = *reinterpret_cast<const X4*>(from + at);
+      if constexpr (kZ) x.b[k] = *reinterpret_cast<const X4*>(from + at + p.k_in);
+    }
+  }
+  // The lane's bias: of its 4 i's, or of its 4 gates and ups.
+  struct Bias {
+    v4f a, b;
+  };
+  __device__ __forceinline__ Bias read_bias(const Tile& t) const {
+    Bias x = {};
+    if (OP == kMmForward && p.bias) {
+      const int lane = here(this->lane);
+      const int i = t.i0 + wi * (kGates ? 32 : 64) + (lane & (kGates ? 7 : 15)) * 4;
+      const int64_t at = (int64_t)t.expert * p.n_out * (kGates ? 2 : 1) + min(i, p.n_out - 4);
+      x.a = load4<DT>(p.bias, at);
+      if (kGates) x.b = load4<DT>(p.bias, at + p.n_out);
+    }
+    return x;
+  }
+  __device__ static v4f wide(const X4& x) {
+    return (v4f){(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
+  }
+
+  // They are turned in 4 KB of LDS, 16 rows at a time, so that 16 lanes hold 64 neighbouring i's of
+  // a row.
   __device__ __forceinline__ void finish(const Tile& t, const v16f& a0, const v16f& a1, int j0,
-                                         uint32_t turn) const {
+                                         uint32_t turn, const Extra& x,
+                                         const Bias& bias) const {
     const int lane = here(this->lane);
     const int rows = min(t.nrows - j0, 32);
     const int64_t row0 = (int64_t)t.row0 + j0;
     auto put = [&](int half_rows) {
       const int l32 = lane & 31, half = lane >> 5;
-      if ((l32 >> 4) != half_rows) return;
+      lanes_fence();
+      if ((l32 >> 4) == half_rows) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {  // i's 32 m + 8 g + 4 half + 0..3 of row l32
-          const v16f& y = m ? a1 : a0;
-          const int piece = 8 * m + 2 * g + half;
-          *(pv4f)(uintptr_t)(turn + (l32 & 15) * 256 + 16 * (piece ^ (l32 & 15))) =
-              (v4f){y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]};
-        }
+          for (int g = 0; g < 4; ++g) {  // i's 32 m + 8 g + 4 half + 0..3 of row l32
+            const v16f& y = m ? a1 : a0;
+            const int piece = 8 * m + 2 * g + half;
+            *(pv4f)(uintptr_t)(turn + (l32 & 15) * 256 + 16 * (piece ^ (l32 & 15))) =
+                (v4f){y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]};
+          }
+      }
+      lanes_fence();
     };
     auto get = [&](int r, int piece) {
       return *(pv4f)(uintptr_t)(turn + (r & 15) * 256 + 16 * (piece ^ (r & 15)));
     };
     if constexpr (kGates) {
       const int i = t.i0 + wi * 32 + (lane & 7) * 4;
-      v4f bg = {}, bu = {};
-      if (p.bias) {
-        const int64_t b = (int64_t)t.expert * 2 * p.n_out + min(i, p.n_out - 4);
-        bg = load4<DT>(p.bias, b);
-        bu = load4<DT>(p.bias, b + p.n_out);
-      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (k % 2 == 0) {
-          lanes_fence();
-          put(k / 2);
-          lanes_fence();
-        }
+        if (k % 2 == 0) put(k / 2);
         const int r = 8 * k + lane / 8;
-        const v4f g = get(r, lane & 7) + bg, u = get(r, 8 + (lane & 7)) + bu;
+        const v4f g = get(r, lane & 7) + bias.a, u = get(r, 8 + (lane & 7)) + bias.b;
         v4f h;
 #pragma unroll
         for (int q = 0; q < 4; ++q) h[q] = g[q] * sigmoid(g[q]) * u[q];
@@ -478,44 +525,26 @@ struct Kernel {
         }
       }
     } else {
-      const int i = t.i0 + wi * 64 + (lane & 15) * 4, safe = min(i, ni() - 4);
-      // what is read comes from the nearest place there is, so that all of it is under way at once
-      constexpr bool kZ = OP == kMmDgrad && SWIGLU;
-      v4f x0[8], x1[kZ ? 8 : 1], b = {};
-      auto at = [&](int k) { return row0 + min(4 * k + lane / 16, rows - 1); };
-      if constexpr (kZ) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          x0[k] = load4<DT>(p.z, at(k) * p.ldz + safe);
-          x1[k] = load4<DT>(p.z, at(k) * p.ldz + p.k_in + safe);
-        }
-      } else if (p.residual) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x0[k] = load4<ODT>(p.residual, at(k) * p.ldres + safe);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x0[k] = b;
-      }
-      if (OP == kMmForward && p.bias) b = load4<DT>(p.bias, (int64_t)t.expert * p.n_out + safe);
+      const int i = t.i0 + wi * 64 + (lane & 15) * 4;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        if (k % 4 == 0) {
-          lanes_fence();
-          put(k / 4);
-          lanes_fence();
-        }
+        if (k % 4 == 0) put(k / 4);
         const int r = 4 * k + lane / 16;
-        const v4f y = get(r, lane & 15);
+        v4f y = get(r, lane & 15);
         const int64_t o = (row0 + r) * p.ldo + i;
         if constexpr (kZ) {
           v4f dg, du;
-          swiglu_gradient(y, x0[k], x1[k], dg, du);
+          swiglu_gradient(y, wide(x.a[k]), wide(x.b[k]), dg, du);
           if (r < rows && i < ni()) {
             store4<ODT>(p.out, o, dg);
             store4<ODT>(p.out, o + p.k_in, du);
           }
         } else {
-          if (r < rows && i < ni()) store4<ODT>(p.out, o, y + b + x0[k]);
+          if constexpr (OP == kMmForward) {
+            y += bias.a;
+            if (p.residual) y += wide(x.a[k]);
+          }
+          if (r < rows && i < ni()) store4<ODT>(p.out, o, y);
         }
       }
     }
@@ -606,8 +635,8 @@ struct Kernel {
     if (q >= end) return;
 
     const uint32_t buf0 = __builtin_amdgcn_readfirstlane(lds_address(lds.buf[0]));
-    Reader<G::BI, G::TI, 1, kPWide> rp;
-    Reader<G::BJ, G::TJ, G::WJ, kQWide> rq;
+    Reader<G::BI, kC, G::TI, 1, kPWide> rp;
+    Reader<G::BJ, kC, G::TJ, G::WJ, kQWide> rq;
     rp.plan(buf0, wi * G::TI, lane);
     rq.plan(buf0 + G::BI * kC * 2, wj, lane);
 
@@ -621,17 +650,17 @@ struct Kernel {
     };
     fetch(d, t, t.row0, t.nc);
     plan(d, t);
+    ahead(d, walk);
     load_all(buf0);
     for (int s = 1; s < kBufs; ++s) {
-      ahead(d, walk);
       advance(d, walk);
       load_all(buf0 + s * G::kBuf);
     }
-    // Stage s + 1 has landed when no more than the loads of two stages, which followed it, are out.
-    constexpr int kKeep = 2 * kLoads;
+    // Stage s + 1 has landed when no more is out than the loads of the kBufs - 2 that followed it.
+    constexpr int kKeep = (kBufs - 2) * kLoads;
     wait_and_barrier<kKeep + kLoads>();
     uint32_t buf = 0;  // the buffer of the stage at work, as an offset
-    // Own turn: three more waits come before the loads that followed a tile's stores.
+    // Own turn: kBufs - 1 waits after a tile's stores are still for loads that went out before them.
     constexpr int kStores = G::TJ * (ODT == kF32 ? 8 : 4);
     int relaxed = 0;
     for (;;) {
@@ -685,16 +714,22 @@ struct Kernel {
           auto nothing = []() {};
           auto no_loads = [](int, int) {};
           Ops now = read(0, buf);
-          // A stage's first operands are read in the second step of the one before, after the
-          // barrier that ends the reads of that one; then its buffer is loaded again.
+          // A stage's first operands are read in the last step of the one before, after the barrier
+          // that ends the reads of that one; then its buffer is loaded again.
           auto stage = [&](auto LOAD) {
             const uint32_t other = (buf + G::kBuf) % (kBufs * G::kBuf);
-            const Ops then = read(1, buf);
+            Ops then = read(1, buf);
+            if constexpr (G::kSteps == 4) {
+              products(now, nothing, no_loads);
+              now = read(2, buf);
+              products(then, nothing, no_loads);
+              then = read(3, buf);
+            }
             if constexpr (OP == kMmWgrad)
               if (sums) sum_columns(sum, buf0 + buf + G::BI * kC * 2);
             products(now, [&]() {
               __builtin_amdgcn_sched_barrier(0);
-              ahead(d, walk);
+              advance(d, walk);
             }, no_loads);
             if (kOwnTurn && relaxed > 0) {
               wait_and_barrier<kKeep + kStores>();
@@ -704,7 +739,6 @@ struct Kernel {
             }
             now = read(0, other);
             if constexpr (decltype(LOAD)::value) {
-              advance(d, walk);
               products(then, nothing, [&](int m, int many) {
 #pragma unroll
                 for (int l = m * kLoads / many; l < (m + 1) * kLoads / many; ++l)
@@ -723,15 +757,21 @@ struct Kernel {
 #pragma unroll
             for (int j = 0; j < NL; ++j)
               finish_own(t, acc[0][j], acc[1][j], (j * G::WJ + wj) * 32, own + 4096 * wave);
-            relaxed = NL == G::TJ ? 3 : 0;
+            relaxed = NL == G::TJ ? kBufs - 1 : 0;
           } else {
             // the results are turned in the buffer that the last stage was in
             for (int left = stages; left > 1; --left) stage(std::true_type());
             const uint32_t turn = buf0 + buf + 4096 * wave;
             stage(std::false_type());
+            const Bias bias = read_bias(t);
+            Extra x, next;
+            if (NL > 0) read_extra(x, t, wj * 32);
 #pragma unroll
-            for (int j = 0; j < NL; ++j)
-              finish(t, acc[0][j], acc[1][j], (j * G::WJ + wj) * 32, turn);
+            for (int j = 0; j < NL; ++j) {
+              if (j + 1 < NL) read_extra(next, t, ((j + 1) * G::WJ + wj) * 32);
+              finish(t, acc[0][j], acc[1][j], (j * G::WJ + wj) * 32, turn, x, bias);
+              x = next;
+            }
           }
         }
       };
@@ -746,7 +786,6 @@ struct Kernel {
       if (q >= end) break;
       if constexpr (!kOwnTurn) {
         barrier();
-        advance(d, walk);
         load_all(buf0 + (buf + (kBufs - 1) * G::kBuf) % (kBufs * G::kBuf));
       }
       t = find(q);
