@@ -572,10 +572,12 @@ def balance_loss_backward(logits, counts, K, grad_logits, valid=None, grad_loss=
 # As above; matrices whose rows may be apart are checked for their type and shape here, too.
 def _matrix(name: str, t, device: int, dtype, shape) -> int:
     """The row stride of a matrix of this type and shape."""
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name}: {dtype} {tuple(shape)} is wanted, not {t.dtype} "
-                         f"{tuple(t.shape)}")
-    return _row_stride(name, t, device)
+    strides = t.stride()
+    if t.dtype != dtype or t.shape != shape or t.get_device() != device or (
+            strides[1] != 1 and shape[1] != 1):
+        raise ValueError(f"{name}: {dtype} {tuple(shape)} of contiguous rows on device {device} is "
+                         f"wanted, not {t.dtype} {tuple(t.shape)} of strides {strides} on {t.device}")
+    return strides[0]
 
 
 def _slots(slot, K: int, T: int, device: int) -> None:

@@ -2,10 +2,11 @@
 // logits, so with gw = d loss / d w
 //   d loss / d logits[t, idx[t, k]] = w_k (gw_k - sum_j w_j gw_j),
 // and 0 for the other experts.  A route whose id is outside [0, E) has no expert row: its gw counts
-// as 0.
+// as 0.  An id that comes twice gets the sum, in the order of k.
 //
-// A wavefront to a token: lane k holds route k, and the row is built in LDS, then written in whole
-// lines.  Bound by those writes.
+// G lanes to a token (16, 32 or 64, K of them with a route), so a wavefront holds 64 / G tokens.  It
+// writes their rows' zeros, which need no input, in 16-byte pieces while the inputs come, waits for
+// them, and writes the K values over them.  Bound by those writes.
 #include "common.hpp"
 #include "train.hpp"
 
@@ -15,37 +16,56 @@ namespace {
 
 constexpr int kWaves = 4;
 
-template <int DT>
+template <int DT, int G>
 __global__ __launch_bounds__(kWaves * 64) void route_backward_kernel(
     const int32_t* __restrict__ idx, const float* __restrict__ w, const float* __restrict__ grad_w,
     int T, int E, int K, bool accumulate, void* grad_logits, int64_t ld) {
   typedef typename Elem<DT>::type V;
-  extern __shared__ float row_lds[];  // [kWaves][E]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int t = blockIdx.x * kWaves + wave;
-  if (t >= T) return;
-  float* row = row_lds + wave * E;
+  constexpr int kVec = 16 / sizeof(V);
+  typedef V vec __attribute__((ext_vector_type(kVec), aligned(sizeof(V))));
+  const int lane = threadIdx.x & 63;
+  const int t0 = (blockIdx.x * kWaves + (threadIdx.x >> 6)) * (64 / G);
+  const int t = t0 + lane / G, k = lane % G;
+  const bool there = t < T && k < K;
   int id = -1;
   float wk = 0.0f, gw = 0.0f;
-  if (lane < K) {
-    id = idx[(int64_t)t * K + lane];
-    wk = w[(int64_t)t * K + lane];
-    if (id >= 0 && id < E) gw = grad_w[(int64_t)t * K + lane];
+  if (there) {
+    const int64_t at = (int64_t)t * K + k;
+    id = idx[at];
+    wk = w[at];
+    gw = grad_w[at];
   }
+  V* const grad = static_cast<V*>(grad_logits);
+  if (!accumulate) {
+    const vec zero = {};
+    const int pieces = E / kVec;
+    for (int x = 0; x < 64 / G && t0 + x < T; ++x) {
+      V* row = grad + (int64_t)(t0 + x) * ld;
+      for (int c = lane; c < pieces; c += 64) *reinterpret_cast<vec*>(row + c * kVec) = zero;
+      const int c = pieces * kVec + lane;
+      if (c < E) row[c] = (V)0.0f;
+    }
+  }
+  const bool on = there && id >= 0 && id < E;
+  if (!on) gw = 0.0f;
   float sum = wk * gw;
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
-  const float d = wk * (gw - sum);
-  // the wavefront's own LDS row, whose operations complete in order
-  for (int e = lane; e < E; e += 64) row[e] = 0.0f;
-  __builtin_amdgcn_wave_barrier();
-  for (int k = 0; k < K; ++k) {  // one by one: an id may come twice
-    if (lane == k && id >= 0 && id < E) row[id] += d;
-    __builtin_amdgcn_wave_barrier();
+  for (int o = G / 2; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
+  const float d = on ? wk * (gw - sum) : 0.0f;
+  float all = 0.0f;  // of the routes with this id
+  for (int j = 0; j < K; ++j) {
+    const int from = (lane & ~(G - 1)) + j;
+    const int other = __shfl(id, from);
+    const float od = __shfl(d, from);
+    all += other == id ? od : 0.0f;
   }
-  V* out = static_cast<V*>(grad_logits) + t * ld;
-  for (int e = lane; e < E; e += 64)
-    out[e] = (V)(accumulate ? (float)out[e] + row[e] : row[e]);
+  V* const to = grad + (int64_t)t * ld + id;
+  if (accumulate) {
+    if (on) all += (float)*to;
+  } else {
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");  // the zeros come first
+  }
+  if (on) *to = (V)all;
 }
 
 }  // namespace
@@ -53,17 +73,25 @@ __global__ __launch_bounds__(kWaves * 64) void route_backward_kernel(
 hipError_t launch_route_backward(const int32_t* idx, const float* w, const float* grad_w, int T,
                                  int E, int K, bool accumulate, void* grad_logits, int dtype,
                                  int64_t ld, hipStream_t s) {
-  const dim3 grid((T + kWaves - 1) / kWaves);
-  const size_t lds = (size_t)kWaves * E * sizeof(float);
-  auto go = [&](auto kernel) {
-    kernel<<<grid, kWaves * 64, lds, s>>>(idx, w, grad_w, T, E, K, accumulate, grad_logits, ld);
+  auto go = [&](auto kernel, int tokens) {
+    const dim3 grid((T + kWaves * tokens - 1) / (kWaves * tokens));
+    kernel<<<grid, kWaves * 64, 0, s>>>(idx, w, grad_w, T, E, K, accumulate, grad_logits, ld);
+  };
+  auto type = [&](auto DT) {
+    constexpr int dt = decltype(DT)::value;
+    if (K <= 16)
+      go(route_backward_kernel<dt, 16>, 4);
+    else if (K <= 32)
+      go(route_backward_kernel<dt, 32>, 2);
+    else
+      go(route_backward_kernel<dt, 64>, 1);
   };
   if (dtype == kF32)
-    go(route_backward_kernel<kF32>);
+    type(std::integral_constant<int, kF32>());
   else if (dtype == kBF16)
-    go(route_backward_kernel<kBF16>);
+    type(std::integral_constant<int, kBF16>());
   else
-    go(route_backward_kernel<kF16>);
+    type(std::integral_constant<int, kF16>());
   return hipGetLastError();
 }
 

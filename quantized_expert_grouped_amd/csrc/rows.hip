@@ -7,8 +7,9 @@
 // multiply-adds, each result is rounded once; no row is looked at that no route names.
 //
 // All are bound by memory.  A thread owns 8 neighbouring columns, and a wavefront lies within one
-// token, whose slots and weights are scalars.  Rows may start at any element: the wide loads and
-// stores need no more than the element's alignment, and only the last H % 8 columns go one by one.
+// row, whose src, or slots and weights, are scalars.  Rows may start at any element: the wide loads
+// and stores need no more than the element's alignment, and only the last H % 8 columns go one by
+// one.  Rows of the experts are read and written once, so past the caches.
 #include <algorithm>
 
 #include "common.hpp"
@@ -20,153 +21,190 @@ namespace {
 
 constexpr int kVec = 8;
 
-template <int DT>
-struct Cols {
-  typedef typename Elem<DT>::type T;
-  typedef T vec __attribute__((ext_vector_type(kVec), aligned(sizeof(T))));
-};
-struct Vals {
-  float v[kVec];
-};
+template <class T>
+using Vec = T __attribute__((ext_vector_type(kVec), aligned(sizeof(T))));
 
-// n of the 8 columns from `at` on are there (uniform but for a row's last thread)
-template <int DT>
-__device__ __forceinline__ typename Cols<DT>::vec load(const void* p, int64_t at, int n) {
-  typedef typename Cols<DT>::T T;
-  typedef typename Cols<DT>::vec vec;
-  const T* q = static_cast<const T*>(p) + at;
-  vec d = {};
-  if (n >= kVec) return *reinterpret_cast<const vec*>(q);
+// 8 columns from p on, of which n are there (all, but for a row's last thread).
+template <class T>
+__device__ __forceinline__ Vec<T> load(const T* p, int n) {
+  if (n >= kVec) return __builtin_nontemporal_load(reinterpret_cast<const Vec<T>*>(p));
+  Vec<T> d = {};
 #pragma unroll
   for (int i = 0; i < kVec - 1; ++i)
-    if (i < n) d[i] = q[i];
+    if (i < n) d[i] = p[i];
   return d;
 }
-template <int DT>
-__device__ __forceinline__ void store(void* p, int64_t at, int n, const Vals& y) {
-  typedef typename Cols<DT>::T T;
-  typedef typename Cols<DT>::vec vec;
-  T* q = static_cast<T*>(p) + at;
-  vec d;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) d[i] = (T)y.v[i];
+template <class T>
+__device__ __forceinline__ void store(T* p, int n, const Vec<T>& d) {
   if (n >= kVec) {
-    *reinterpret_cast<vec*>(q) = d;
+    __builtin_nontemporal_store(d, reinterpret_cast<Vec<T>*>(p));
     return;
   }
 #pragma unroll
   for (int i = 0; i < kVec - 1; ++i)
-    if (i < n) q[i] = d[i];
+    if (i < n) p[i] = d[i];
+}
+template <class T>
+__device__ __forceinline__ Vec<T> rounded(const float (&y)[kVec]) {
+  Vec<T> d;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) d[i] = (T)y[i];
+  return d;
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
-// V: the values' bits
-template <class V>
-__global__ __launch_bounds__(256) void dispatch_kernel(DispatchArgs a) {
-  typedef V vec __attribute__((ext_vector_type(kVec), aligned(sizeof(V))));
-  const int r = uniform(blockIdx.x * blockDim.y + threadIdx.y);
-  if (r >= a.rows) return;
-  const int v = a.src[r], t = v / a.K;
-  if (v < 0 || t >= a.T) return;
-  const V* x = static_cast<const V*>(a.x) + t * a.ldx;
-  V* out = static_cast<V*>(a.out) + r * a.ldo;
-  for (int c = (blockIdx.y * blockDim.x + threadIdx.x) * kVec; c < a.H;
-       c += gridDim.y * blockDim.x * kVec) {
-    if (c + kVec <= a.H)
-      *reinterpret_cast<vec*>(out + c) = *reinterpret_cast<const vec*>(x + c);
-    else
-      for (int i = c; i < a.H; ++i) out[i] = x[i];
-  }
+// what a wavefront's scalars are read by, whatever is written meanwhile
+template <class T>
+using Scalars = const __attribute__((address_space(4))) T*;
+template <class T>
+__device__ __forceinline__ Scalars<T> scalars(const T* p) {
+  return (Scalars<T>)(uintptr_t)p;
 }
 
-constexpr int kBatch = 8;  // rows whose loads are under way together
-
-template <int DT, int ODT>
-__global__ __launch_bounds__(256) void combine_rows_kernel(CombineArgs a) {
-  const int t = uniform(blockIdx.x * blockDim.y + threadIdx.y);
-  if (t >= a.T) return;
-  const int32_t* slot = a.slot + (int64_t)t * a.K;
-  const float* w = a.w ? a.w + (int64_t)t * a.K : nullptr;
+// kRows rows a thread, whose loads are under way together (8192 tokens, K = 10, H = 2048, bf16: one
+// row a thread 85 us).  V: the values' bits.
+template <class V, int kRows>
+__global__ __launch_bounds__(256) void dispatch_kernel(DispatchArgs a) {
+  const int r0 = uniform((blockIdx.x * blockDim.y + threadIdx.y) * kRows);
+  int t[kRows];
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    const int v = scalars(a.src)[min(r0 + j, a.rows - 1)];
+    t[j] = r0 + j >= a.rows || v < 0 || v / a.K >= a.T ? -1 : v / a.K;
+  }
+  const V* x = static_cast<const V*>(a.x);
+  V* out = static_cast<V*>(a.out);
   for (int c = (blockIdx.y * blockDim.x + threadIdx.x) * kVec; c < a.H;
        c += gridDim.y * blockDim.x * kVec) {
     const int n = a.H - c;
-    Vals acc = {};
-    if (a.residual) {
-      const auto d = load<ODT>(a.residual, t * a.ldres + c, n);
+    Vec<V> d[kRows];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) acc.v[i] = (float)d[i];
+    for (int j = 0; j < kRows; ++j) {
+      const V* from = x + max(t[j], 0) * a.ldx + c;  // read K times: through the caches
+      d[j] = n >= kVec ? *reinterpret_cast<const Vec<V>*>(from) : load(from, n);
     }
-    for (int k0 = 0; k0 < a.K; k0 += kBatch) {
-      typename Cols<DT>::vec d[kBatch];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (k0 + j < a.K && (uint32_t)slot[k0 + j] < (uint32_t)a.n_rows)  // uniform
-          d[j] = load<DT>(a.rows, slot[k0 + j] * a.ldr + c, n);
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (k0 + j < a.K && (uint32_t)slot[k0 + j] < (uint32_t)a.n_rows) {
-          const float wk = w ? w[k0 + j] : 1.0f;
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) acc.v[i] = fmaf(wk, (float)d[j][i], acc.v[i]);
-        }
-    }
-    store<ODT>(a.out, t * a.ldo + c, n, acc);
+    for (int j = 0; j < kRows; ++j)
+      if (t[j] >= 0) store(out + (r0 + j) * a.ldo + c, n, d[j]);
   }
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+// Routes whose rows' loads are under way together.
+template <int DT>
+constexpr int kBatch = DT == kF32 ? 8 : 16;
+
+template <int DT, int ODT>
+__global__ __launch_bounds__(256) void combine_rows_kernel(CombineArgs a) {
+  typedef typename Elem<DT>::type T;
+  typedef typename Elem<ODT>::type OT;
+  constexpr int kB = kBatch<DT>;
+  const int t = uniform(blockIdx.x * blockDim.y + threadIdx.y);
+  if (t >= a.T) return;
+  const auto slot = scalars(a.slot) + (int64_t)t * a.K;
+  const auto w = scalars(a.w) + (a.w ? (int64_t)t * a.K : 0);
+  const T* rows = static_cast<const T*>(a.rows);
+  for (int c = (blockIdx.y * blockDim.x + threadIdx.x) * kVec; c < a.H;
+       c += gridDim.y * blockDim.x * kVec) {
+    const int n = a.H - c;
+    float acc[kVec] = {};
+    if (a.residual) {
+      const Vec<OT> d = load(static_cast<const OT*>(a.residual) + t * a.ldres + c, n);
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+      for (int i = 0; i < kVec; ++i) acc[i] = (float)d[i];
+    }
+    for (int k0 = 0; k0 < a.K; k0 += kB) {
+      Vec<T> d[kB];
+#pragma unroll
+      for (int j = 0; j < kB; ++j)
+        if (k0 + j < a.K && (uint32_t)slot[k0 + j] < (uint32_t)a.n_rows)  // uniform
+          d[j] = load(rows + slot[k0 + j] * a.ldr + c, n);
+#pragma unroll
+      for (int j = 0; j < kB; ++j)
+        if (k0 + j < a.K && (uint32_t)slot[k0 + j] < (uint32_t)a.n_rows) {
+          const float wk = a.w ? w[k0 + j] : 1.0f;
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) acc[i] = fmaf(wk, (float)d[j][i], acc[i]);
+        }
+    }
+    store(static_cast<OT*>(a.out) + t * a.ldo + c, n, rounded<OT>(acc));
+  }
 }
 
-// A workgroup of blockDim.x threads to a token.
+// The wavefront's sum, in all lanes: DPP steps leave each row of 16 lanes with its row's, then the
+// four rows' are read into scalars.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<0xB1>(v);   // quad_perm [1, 0, 3, 2]
+  v += dpp<0x4E>(v);   // quad_perm [2, 3, 0, 1]
+  v += dpp<0x141>(v);  // lane i <-> 7 - i within each half row
+  v += dpp<0x140>(v);  // lane i <-> 15 - i within each row
+  auto row = [&](int i) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16 * i));
+  };
+  return (row(0) + row(1)) + (row(2) + row(3));
+}
+
+// A workgroup of blockDim.x threads to a token (a wavefront to a token: 199 us instead of 148 at 8192
+// tokens, K = 10, H = 2048, bf16 rows, fp32 gradients).
 template <int DT, int GDT>
 __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBackwardArgs a) {
-  __shared__ float part[4][kBatch];
-  const int t = blockIdx.x, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  const int32_t* slot = a.slot + (int64_t)t * a.K;
-  const float* w = a.w ? a.w + (int64_t)t * a.K : nullptr;
-  for (int k0 = 0; k0 < a.K; k0 += kBatch) {
-    float dot[kBatch];
+  typedef typename Elem<DT>::type T;
+  typedef typename Elem<GDT>::type GT;
+  constexpr int kB = kBatch<DT>;
+  __shared__ float part[4][kB];
+  const int wave = uniform(threadIdx.x >> 6), waves = blockDim.x >> 6, t = blockIdx.x;
+  const auto slot = scalars(a.slot) + (int64_t)t * a.K;
+  const auto w = scalars(a.w) + (a.w ? (int64_t)t * a.K : 0);
+  const T* rows = static_cast<const T*>(a.rows);
+  T* grad_rows = static_cast<T*>(a.grad_rows);
+  for (int k0 = 0; k0 < a.K; k0 += kB) {
+    float dot[kB];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) dot[j] = 0.0f;
+    for (int j = 0; j < kB; ++j) dot[j] = 0.0f;
     for (int c = threadIdx.x * kVec; c < a.H; c += blockDim.x * kVec) {
       const int n = a.H - c;
-      const auto g = load<GDT>(a.grad_out, t * a.ldg + c, n);
-      typename Cols<DT>::vec d[kBatch];
+      Vec<T> d[kB];
       if (a.grad_w)
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
+        for (int j = 0; j < kB; ++j)
           if (k0 + j < a.K && (uint32_t)slot[k0 + j] < (uint32_t)a.n_rows)
-            d[j] = load<DT>(a.rows, slot[k0 + j] * a.ldr + c, n);
+            d[j] = load(rows + slot[k0 + j] * a.ldr + c, n);
+      const Vec<GT> gv = load(static_cast<const GT*>(a.grad_out) + t * a.ldg + c, n);
+      float g[kVec];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
+      for (int i = 0; i < kVec; ++i) g[i] = (float)gv[i];
+#pragma unroll
+      for (int j = 0; j < kB; ++j)
         if (k0 + j < a.K && (uint32_t)slot[k0 + j] < (uint32_t)a.n_rows) {
           if (a.grad_w)
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) dot[j] = fmaf((float)g[i], (float)d[j][i], dot[j]);
-          if (a.grad_rows) {
-            const float wk = w ? w[k0 + j] : 1.0f;
-            Vals y;
+            for (int i = 0; i < kVec; ++i) dot[j] = fmaf(g[i], (float)d[j][i], dot[j]);
+          if (grad_rows) {
+            const float wk = a.w ? w[k0 + j] : 1.0f;
+            float y[kVec];
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) y.v[i] = wk * (float)g[i];
-            store<DT>(a.grad_rows, slot[k0 + j] * a.ldgr + c, n, y);
+            for (int i = 0; i < kVec; ++i) y[i] = wk * g[i];
+            store(grad_rows + slot[k0 + j] * a.ldgr + c, n, rounded<T>(y));
           }
         }
     }
     if (!a.grad_w) continue;
+    float* to = a.grad_w + (int64_t)t * a.K + k0;
+    const int many = min(kB, a.K - k0);
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      dot[j] = wave_sum(dot[j]);
-      if ((threadIdx.x & 63) == 0) part[wave][j] = dot[j];
+    for (int j = 0; j < kB; ++j) {
+      if (j >= many) break;  // uniform
+      const float s = wave_sum(dot[j]);
+      if ((threadIdx.x & 63) == 0) part[wave][j] = s;
     }
     __syncthreads();
-    if (threadIdx.x < kBatch && k0 + threadIdx.x < a.K) {
+    if ((int)threadIdx.x < many) {
       float s = part[0][threadIdx.x];
       for (int i = 1; i < waves; ++i) s += part[i][threadIdx.x];
-      a.grad_w[(int64_t)t * a.K + k0 + threadIdx.x] = s;
+      to[threadIdx.x] = s;
     }
     __syncthreads();
   }
@@ -180,25 +218,41 @@ int row_threads(int H) {
 struct Shape {
   dim3 grid, block;
 };
-Shape shape_of(int rows, int H) {
-  const int x = row_threads(H), y = 256 / x;
+Shape shape_of(int rows, int H, int rows_a_thread) {
+  const int x = row_threads(H), y = 256 / x, high = y * rows_a_thread;
   const int chunks = (H + kVec * x - 1) / (kVec * x);
-  return {dim3((rows + y - 1) / y, std::min(chunks, 64)), dim3(x, y)};
+  return {dim3((rows + high - 1) / high, std::min(chunks, 64)), dim3(x, y)};
+}
+
+template <class V>
+void dispatch(const DispatchArgs& a, hipStream_t s) {
+  // few rows: one a thread, for more workgroups (a batch of 17 tokens, K = 10)
+  if (a.rows < 4096) {
+    const Shape g = shape_of(a.rows, a.H, 1);
+    dispatch_kernel<V, 1><<<g.grid, g.block, 0, s>>>(a);
+  } else {
+    const Shape g = shape_of(a.rows, a.H, 4);
+    dispatch_kernel<V, 4><<<g.grid, g.block, 0, s>>>(a);
+  }
+}
+
+template <int DT, int GDT>
+void backward(const CombineBackwardArgs& a, hipStream_t s) {
+  combine_backward_kernel<DT, GDT><<<a.T, row_threads(a.H), 0, s>>>(a);
 }
 
 }  // namespace
 
 hipError_t launch_dispatch_rows(const DispatchArgs& a, hipStream_t s) {
-  const Shape g = shape_of(a.rows, a.H);
   if (a.dtype == kF32)
-    dispatch_kernel<uint32_t><<<g.grid, g.block, 0, s>>>(a);
+    dispatch<uint32_t>(a, s);
   else
-    dispatch_kernel<uint16_t><<<g.grid, g.block, 0, s>>>(a);
+    dispatch<uint16_t>(a, s);
   return hipGetLastError();
 }
 
 hipError_t launch_combine_rows(const CombineArgs& a, hipStream_t s) {
-  const Shape g = shape_of(a.T, a.H);
+  const Shape g = shape_of(a.T, a.H, 1);
   if (a.dtype == kF32)
     combine_rows_kernel<kF32, kF32><<<g.grid, g.block, 0, s>>>(a);
   else if (a.dtype == kBF16 && a.out_dtype == kF32)
@@ -213,17 +267,16 @@ hipError_t launch_combine_rows(const CombineArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_combine_rows_backward(const CombineBackwardArgs& a, hipStream_t s) {
-  const int threads = row_threads(a.H);
   if (a.dtype == kF32)
-    combine_backward_kernel<kF32, kF32><<<a.T, threads, 0, s>>>(a);
+    backward<kF32, kF32>(a, s);
   else if (a.dtype == kBF16 && a.grad_dtype == kF32)
-    combine_backward_kernel<kBF16, kF32><<<a.T, threads, 0, s>>>(a);
+    backward<kBF16, kF32>(a, s);
   else if (a.dtype == kBF16)
-    combine_backward_kernel<kBF16, kBF16><<<a.T, threads, 0, s>>>(a);
+    backward<kBF16, kBF16>(a, s);
   else if (a.grad_dtype == kF32)
-    combine_backward_kernel<kF16, kF32><<<a.T, threads, 0, s>>>(a);
+    backward<kF16, kF32>(a, s);
   else
-    combine_backward_kernel<kF16, kF16><<<a.T, threads, 0, s>>>(a);
+    backward<kF16, kF16>(a, s);
   return hipGetLastError();
 }
 
