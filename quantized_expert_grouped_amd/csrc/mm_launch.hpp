@@ -21,7 +21,7 @@ template <class G>
 int64_t most_tiles(const MmProblem& p) {
   const int feat = p.op == kMmForward && p.swiglu ? G::BI / 2 : G::BI;
   const int64_t ni = ((p.op == kMmForward ? p.n_out : p.k_in) + feat - 1) / feat;
-  if (p.op == kMmWgrad) return ni * ((p.n_out + G::BJ - 1) / G::BJ) * p.E;
+  if (p.op == kMmWgrad) return ni * ((p.n_out + G::BJ - 1) / G::BJ) * p.E * p.parts;
   return ni * (p.rows / G::BJ + std::min(p.E, p.rows));
 }
 

@@ -219,7 +219,7 @@ struct Kernel {
     ni_tiles = (uint32_t)(ni() + kFeat - 1) / kFeat;
     if constexpr (OP == kMmWgrad) {
       per_expert = (uint32_t)(p.n_out + G::BJ - 1) / G::BJ;
-      nj_tiles = (uint32_t)p.E * per_expert;
+      nj_tiles = (uint32_t)p.E * (uint32_t)p.parts * per_expert;
       return nj_tiles * ni_tiles;
     } else {
       for (int e = threadIdx.x; e <= p.E; e += G::kWaves * 64)
@@ -248,10 +248,17 @@ struct Kernel {
     int qr = (int)(g * kGroup + in - qi * high);
     t.i0 = qi * kFeat;
     if constexpr (OP == kMmWgrad) {
-      t.expert = qr / (int)per_expert;
+      t.expert = qr / (int)per_expert;  // of p.parts to an expert, each with a part of its rows
       t.j0 = (qr - t.expert * (int)per_expert) * G::BJ;
-      t.row0 = min(constant(p.offsets)[t.expert], p.rows);
-      t.nc = max(min(constant(p.offsets)[t.expert + 1], p.rows) - t.row0, 0);
+      const int e = p.parts > 1 ? t.expert / p.parts : t.expert;
+      t.row0 = min(constant(p.offsets)[e], p.rows);
+      t.nc = max(min(constant(p.offsets)[e + 1], p.rows) - t.row0, 0);
+      if (p.parts > 1) {
+        const int part = ((t.nc + p.parts - 1) / p.parts + kC - 1) / kC * kC;
+        const int at = min((t.expert - e * p.parts) * part, t.nc);
+        t.row0 += at;
+        t.nc = min(t.nc - at, part);
+      }
       t.nrows = min(p.n_out - t.j0, G::BJ);
     } else {
       const int s = __popcll(ballot(before <= qr)) - 1;  // the last segment that is not past it

@@ -75,6 +75,7 @@ struct MmProblem {
   int64_t ldo;
   void* bias_out;          // wgrad: [E x n_out] of out's type, or nullptr
   int n_out, k_in, E, n_act, K, rows;
+  int parts;               // wgrad: of each expert's rows, out and bias_out having [E x parts]
   uint32_t k_mul, k_shift;  // division by K (set_division)
 };
 // n / K = n * k_mul >> k_shift for n < 2^30, K <= 64: k_mul K - 2^k_shift <= K <= 2^(k_shift - 30)
