@@ -32,19 +32,28 @@ hipError_t launch_geo(const MmProblem& p, hipStream_t s) {
   mm_kernel<OP, DT, ODT, SWIGLU, G><<<grid, G::kWaves * 64, 0, s>>>(p);
   return hipGetLastError();
 }
-// 256 x 256, and 128 x 128 with two workgroups a CU.  In stages of 64 a narrow operand's rows come in
-// whole 128-byte lines; wgrad has none, and its short tiles like more loads on their way.
+// 256 x 256; 128 x 128 with two workgroups a CU; and 128 x 128 with one, where there are no more tiles
+// than CUs, and buffers for as many loads on their way as LDS has room for.  In stages of 64 a narrow
+// operand's rows come in whole 128-byte lines; wgrad has none, and its short tiles like more loads
+// on their way.
 template <int OP>
-using Large = tile::Geo<4, 2, 2, 4, OP == kMmWgrad ? 32 : 64>;
+using Large = tile::Geo<4, 2, 2, 4, OP == kMmWgrad ? 32 : 64, OP == kMmWgrad ? 4 : 2>;
 template <int OP>
-using Small = tile::Geo<2, 2, 2, 2, OP == kMmWgrad ? 32 : 64>;
+using Small = tile::Geo<2, 2, 2, 2, OP == kMmWgrad ? 32 : 64, OP == kMmWgrad ? 4 : 2>;
+template <int OP>
+using Deep = tile::Geo<2, 2, 2, 2, 64, 4>;
 
 template <int OP, int DT, int ODT, bool SWIGLU>
+hipError_t launch_small(const MmProblem& p, hipStream_t s) {
+  return most_tiles<Small<OP>>(p) <= kCus ? launch_geo<OP, DT, ODT, SWIGLU, Deep<OP>>(p, s)
+                                          : launch_geo<OP, DT, ODT, SWIGLU, Small<OP>>(p, s);
+}
+template <int OP, int DT, int ODT, bool SWIGLU>
 hipError_t launch_tiles(const MmProblem& p, hipStream_t s) {
-  const bool few_rows = OP != kMmWgrad && p.rows / p.E <= 64;
+  const bool few_rows = p.rows / p.E <= 64;
   return most_tiles<Large<OP>>(p) >= kCus && !few_rows
              ? launch_geo<OP, DT, ODT, SWIGLU, Large<OP>>(p, s)
-             : launch_geo<OP, DT, ODT, SWIGLU, Small<OP>>(p, s);
+             : launch_small<OP, DT, ODT, SWIGLU>(p, s);
 }
 
 }  // namespace moe

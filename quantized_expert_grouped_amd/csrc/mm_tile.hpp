@@ -1,7 +1,7 @@
 // The grouped products' tile kernel: D[i, j] = sum_c P[i, c] Q[j, c] for a tile of BI x BJ results
 // at a time, c in stages of 32 or 64.
 //
-// A stage of an operand goes from memory straight into one of four or two LDS buffers
+// A stage of an operand goes from memory straight into one of two or four LDS buffers
 // (buffer_load_dwordx4 ... lds).  An operand whose c is contiguous in memory (w and a in the
 // forward, grad in dgrad) lies there as rows of a stage's c; one whose i or j is contiguous (w
 // in dgrad, both in wgrad) as a stage's rows of BI or BJ values, and is turned by the LDS read itself
@@ -30,17 +30,17 @@ __device__ __forceinline__ uint32_t none_if(bool none) { return none ? kNone : 0
 
 // Wavefronts: WI slices of i by WJ of j, each TI x TJ MFMA tiles of 32 x 32; j's tiles are dealt to
 // the WJ in turn, so that few rows still keep all busy.  C c's make a stage, a step of the matrix
-// instruction 16 of them.
-template <int WI_, int WJ_, int TI_, int TJ_, int C_>
+// instruction 16 of them; BUFS stages have buffers.
+template <int WI_, int WJ_, int TI_, int TJ_, int C_, int BUFS_>
 struct Geo {
-  static constexpr int WI = WI_, WJ = WJ_, TI = TI_, TJ = TJ_, kC = C_, kBufs = 128 / C_;
+  static constexpr int WI = WI_, WJ = WJ_, TI = TI_, TJ = TJ_, kC = C_, kBufs = BUFS_;
   static constexpr int kSteps = kC / 16, kPieces = kC / 8;  // of a narrow row
   static constexpr int kWaves = WI * WJ, BI = WI * TI * 32, BJ = WJ * TJ * 32;
   static constexpr int kPL = BI * kC / 512 / kWaves, kQL = BJ * kC / 512 / kWaves;  // loads of 1 KB
   static constexpr int kBuf = (BI + BJ) * kC * 2;
-  static constexpr int kPerCu = kWaves >= 8 ? 1 : 2;  // workgroups of a CU
+  static constexpr int kPerCu = kBufs * kBuf > 65536 ? 1 : 2;  // workgroups of a CU
   static_assert(TI == 2 && BI * kC % (512 * kWaves) == 0 && BJ * kC % (512 * kWaves) == 0 &&
-                    (kC == 32 || kC == 64),
+                    (kC == 32 || kC == 64) && kBufs >= 2,
                 "whole loads");
   static_assert((BI & (BI - 1)) == 0 && (BJ & (BJ - 1)) == 0 && kBuf >= kWaves * 4096, "layout");
 };

@@ -59,7 +59,7 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ w,
 template <int DT, int ODT>
 hipError_t run(const MmProblem& p, bool large, hipStream_t s) {
   return large ? launch_geo<kMmWgrad, DT, ODT, false, Large<kMmWgrad>>(p, s)
-               : launch_geo<kMmWgrad, DT, ODT, false, Small<kMmWgrad>>(p, s);
+               : launch_small<kMmWgrad, DT, ODT, false>(p, s);
 }
 template <int DT>
 hipError_t wgrad(MmProblem p, void* ws, hipStream_t s) {
