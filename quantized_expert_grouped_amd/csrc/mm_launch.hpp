@@ -32,10 +32,13 @@ hipError_t launch_geo(const MmProblem& p, hipStream_t s) {
   mm_kernel<OP, DT, ODT, SWIGLU, G><<<grid, G::kWaves * 64, 0, s>>>(p);
   return hipGetLastError();
 }
-// 256 x 256; 128 x 128 with two workgroups a CU; and 128 x 128 with one, where there are no more tiles
-// than CUs, and buffers for as many loads on their way as LDS has room for.  In stages of 64 a narrow
-// operand's rows come in whole 128-byte lines; wgrad has none, and its short tiles like more loads
-// on their way.
+// 256 x 256; 128 x 128 with two workgroups a CU; and, but for wgrad, 128 x 128 with one, where there
+// are no more tiles than CUs, and buffers for as many loads on their way as LDS has room for (128 rows,
+// 4096 -> 4096: 43 us with two buffers, 38 with four; wgrad of 75 rows in the mean 14.5, 18.9).  In
+// stages of 64 a narrow operand's rows come in whole 128-byte lines; wgrad has none, and its short
+// tiles like more loads on their way (8191 x 4096 x 4096, and 8192 tokens over 512 experts' 2 x 512 x
+// 2048, in us: forward 242 and 585 with stages of 64, 250 and 604 of 32; dgrad 243, 582 and 247, 566;
+// wgrad 238, 809 and 239, 779).
 template <int OP>
 using Large = tile::Geo<4, 2, 2, 4, OP == kMmWgrad ? 32 : 64, OP == kMmWgrad ? 4 : 2>;
 template <int OP>
@@ -45,9 +48,12 @@ using Deep = tile::Geo<2, 2, 2, 2, 64, 4>;
 
 template <int OP, int DT, int ODT, bool SWIGLU>
 hipError_t launch_small(const MmProblem& p, hipStream_t s) {
-  return most_tiles<Small<OP>>(p) <= kCus ? launch_geo<OP, DT, ODT, SWIGLU, Deep<OP>>(p, s)
-                                          : launch_geo<OP, DT, ODT, SWIGLU, Small<OP>>(p, s);
+  if constexpr (OP != kMmWgrad)
+    if (most_tiles<Small<OP>>(p) <= kCus) return launch_geo<OP, DT, ODT, SWIGLU, Deep<OP>>(p, s);
+  return launch_geo<OP, DT, ODT, SWIGLU, Small<OP>>(p, s);
 }
+// Large where it fills the CUs and an expert has more than 64 rows in the mean (2048 -> 2 x 512, 512
+// experts, 40 rows each: 400 us in 128 x 128, 433 in 256 x 256; 160 rows: 722, 585).
 template <int OP, int DT, int ODT, bool SWIGLU>
 hipError_t launch_tiles(const MmProblem& p, hipStream_t s) {
   const bool few_rows = p.rows / p.E <= 64;

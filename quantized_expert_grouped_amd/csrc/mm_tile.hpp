@@ -429,11 +429,12 @@ struct Kernel {
   __device__ __forceinline__ void ahead(Loads& d, Walk& k) const {
     if (d.left <= kC) {  // the next stage is another tile's
       k.q += k.step;
-      if (k.q < k.end)
+      if (k.q < k.end) {
         k.next = find(k.q);
-      else
+        fetch(d, k.next, k.next.row0, k.next.nc);
+      } else {
         k.next.nc = 0;  // a tile of nothing: its loads fetch nothing
-      fetch(d, k.next, k.next.row0, k.next.nc);
+      }
     } else if (OP == kMmWgrad) {
       fetch(d, k.next, d.row + kC, d.left - kC);
     }

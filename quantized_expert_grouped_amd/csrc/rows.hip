@@ -196,9 +196,10 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBackwardAr
     const int many = min(kB, a.K - k0);
 #pragma unroll
     for (int j = 0; j < kB; ++j) {
-      if (j >= many) break;  // uniform
-      const float s = wave_sum(dot[j]);
-      if ((threadIdx.x & 63) == 0) part[wave][j] = s;
+      if (j < many) {  // uniform
+        const float s = wave_sum(dot[j]);
+        if ((threadIdx.x & 63) == 0) part[wave][j] = s;
+      }
     }
     __syncthreads();
     if ((int)threadIdx.x < many) {
