@@ -8,7 +8,7 @@
 namespace moe {
 
 template <int OP, int DT, int ODT, bool SWIGLU, class G>
-__global__ __launch_bounds__(G::kWaves * 64, 2) void mm_kernel(MmProblem p) {
+__global__ __launch_bounds__(G::kWaves * 64, G::kWaves * G::kPerCu / 4) void mm_kernel(MmProblem p) {
   typedef tile::Kernel<OP, DT, ODT, SWIGLU, G> K;
   __shared__ typename K::L lds;
   K(p, lds).run();

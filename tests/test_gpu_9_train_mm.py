@@ -22,6 +22,11 @@ SHAPES = [
     (1000, 1, 1, 384, 1160, False, 0.0, 0.0, 24), (2500, 2, 9, 136, 648, False, 0.4, 0.3, 0),
     (900, 1, 1, 1032, 64, False, 0.0, 0.0, 0), (2100, 1, 1, 520, 2056, True, 0.0, 0.0, 8),
     (513, 4, 5, 768, 328, True, 0.5, 0.0, 0), (40, 2, 3, 64, 64, True, 0.0, 1.0, 0),
+    # more experts than lanes in the tiles of each size; workgroups that walk through several tiles; parts of
+    # an expert's rows; tiles of more rows than one
+    (2000, 4, 300, 72, 200, True, 0.3, 0.0, 0), (3000, 4, 130, 264, 136, True, 0.2, 0.1, 8),
+    (1600, 4, 64, 1024, 1032, True, 0.5, 0.1, 0), (1600, 4, 64, 1032, 1024, False, 0.5, 0.1, 0),
+    (6000, 2, 3, 328, 200, True, 0.6, 0.0, 0), (5000, 1, 1, 2056, 264, False, 0.0, 0.0, 0),
 ]
 
 
