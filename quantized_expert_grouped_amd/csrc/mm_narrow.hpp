@@ -160,11 +160,11 @@ inline int columns(const MmProblem& p) { return (p.n_out + kCols - 1) / kCols; }
 // Whether it beats the 128 x 128 tiles, by sizes alone.  It reads a matrix once for each 16 rows, at
 // about 4.5 TB/s and 5 us more; a tile of few rows takes 12 us for each 1024 of k, however few there
 // are, and reads a matrix once (us, narrow and tiles; rows spread over E experts):
-//   4096 -> 4096, E = 1         1 row 10, 48;  16 rows 20, 49;  64 rows 46, 51;  128 rows 81, 43
-//   2048 -> 2048, E = 8         2 rows 7, 26;  64 rows 26, 28;  128 rows 39, 29
-//   1024 -> 1024, E = 64        8 rows 6, 15;  16 rows 10, 16;  32 rows 17, 17;  64 rows 30, 18
-//   512 -> 2048, E = 512        10 rows 8.5, 11.5;  20 rows 15, 13;  80 rows 52, 38
-//   2048 -> 2 x 512, E = 512    10 rows 15, 23;  80 rows 67, 85;  160 rows 119, 128;  320 rows 221, 187
+//   4096 -> 4096, E = 1         1 row 10, 50;  16 rows 20, 51;  64 rows 46, 53;  128 rows 81, 39
+//   2048 -> 2048, E = 8         2 rows 7, 27;  64 rows 27, 29;  128 rows 40, 30
+//   1024 -> 1024, E = 64        8 rows 7, 16;  16 rows 12, 17;  32 rows 19, 18;  64 rows 34, 18
+//   512 -> 2048, E = 512        10 rows 9, 12;  20 rows 17, 13;  80 rows 55, 38
+//   2048 -> 2 x 512, E = 512    10 rows 16, 19;  80 rows 69, 85;  160 rows 122, 128;  320 rows 227, 187
 inline bool wins(const MmProblem& p) {
   if (columns(p) > 65535) return false;
   const int64_t tiles = std::min(p.rows, p.E) + p.rows / kRows;

@@ -10,10 +10,10 @@
 // A piece that is not there (past the matrix's edge, the last row, the end of c) has an offset past
 // the buffer descriptor's size, for which the load writes zeros without a fetch.
 //
-// What bounds it (us, MI355X): 8191 x 4096 x 4096 forward 242 (1136 TFLOP/s; the matrix cores are busy
-// for 66% of the cycles, LDS reads find no bank conflict), dgrad 226 to 243, wgrad 236 to 243; 8192
-// tokens, K = 10, 512 experts, 2048 -> 2 x 512: memory, 2.4 GB in 547 to 590, dgrad 579, wgrad 772
-// with 2.1 GB to write.
+// What bounds it (us, MI355X): 8191 x 4096 x 4096 forward 237 to 243 (1130 to 1160 TFLOP/s; the matrix
+// cores are busy for 61% of the cycles, LDS reads find no bank conflict), dgrad 226 to 243, wgrad 242
+// to 250; 8192 tokens, K = 10, 512 experts, 2048 -> 2 x 512: memory, 2.4 GB in 547 to 590, dgrad 577,
+// wgrad 780 with 2.1 GB to write.
 //
 // Workgroups stay and walk through the tiles.  Loads run as many stages ahead of the products as
 // there are buffers, over the tiles' ends: a stage's go out into the buffer whose reads have just

@@ -6,7 +6,7 @@
 //
 // G lanes to a token (16, 32 or 64, K of them with a route), so a wavefront holds 64 / G tokens.  It
 // writes their rows' zeros, which need no input, in 16-byte pieces while the inputs come, waits for
-// them, and writes the K values over them.  Bound by those writes.
+// them, and writes the K values over them.  Bound by those writes (30118 x 512 bf16, 31 MB: 9.3 us).
 #include "common.hpp"
 #include "train.hpp"
 

@@ -61,8 +61,9 @@ __device__ __forceinline__ Scalars<T> scalars(const T* p) {
   return (Scalars<T>)(uintptr_t)p;
 }
 
-// kRows rows a thread, whose loads are under way together (8192 tokens, K = 10, H = 2048, bf16: one
-// row a thread 85 us).  V: the values' bits.
+// kRows rows a thread, whose loads are under way together.  Bound by memory: 73,800 rows of 2048 bf16
+// of 8192 tokens take 84 us, 604 MB read and written, the reads mostly from the memory-side cache.
+// V: the values' bits.
 template <class V, int kRows>
 __global__ __launch_bounds__(256) void dispatch_kernel(DispatchArgs a) {
   const int r0 = uniform((blockIdx.x * blockDim.y + threadIdx.y) * kRows);
@@ -148,7 +149,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // A workgroup of blockDim.x threads to a token (a wavefront to a token: 199 us instead of 148 at 8192
-// tokens, K = 10, H = 2048, bf16 rows, fp32 gradients).
+// tokens, K = 10, H = 2048, bf16 rows, fp32 gradients).  Bound by memory: 738 MB, 5.0 TB/s.
 template <int DT, int GDT>
 __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBackwardArgs a) {
   typedef typename Elem<DT>::type T;
