@@ -588,8 +588,8 @@ int moe_mm_grouped_wgrad(const void *grad, int dtype, int64_t ldg, int n_out, co
 /* The gradient of moe_route_topk's logits from grad_w [T x K], its weights':
  *   grad_logits[t, topk_idx[t, k]] = w_k (gw_k - sum_j w_j gw_j), 0 for the other experts,
  * rows of E values of `dtype`, ld apart, in fp32 and rounded once; accumulate != 0 adds it to what
- * grad_logits holds (moe_balance_loss_backward's gradient, say).  The gw of a route whose id is
- * outside [0, E) counts as 0.  T <= 2^23. */
+ * grad_logits holds (moe_balance_loss_backward's gradient, say).  The w and gw of a route whose id
+ * is outside [0, E) are not looked at: w gw counts as 0.  T <= 2^23. */
 int moe_route_topk_backward(const int32_t *topk_idx, const float *topk_w, const float *grad_w,
                             int T, int E, int K, int accumulate, void *grad_logits, int dtype,
                             int64_t ld, void *stream);

@@ -1,8 +1,8 @@
 // The gradient of the router's logits.  The K routing weights are the softmax of the K chosen
 // logits, so with gw = d loss / d w
 //   d loss / d logits[t, idx[t, k]] = w_k (gw_k - sum_j w_j gw_j),
-// and 0 for the other experts.  A route whose id is outside [0, E) has no expert row: its gw counts
-// as 0.  An id that comes twice gets the sum, in the order of k.
+// and 0 for the other experts.  A route whose id is outside [0, E) has no expert row: w_k gw_k
+// counts as 0, whatever the two are.  An id that comes twice gets the sum, in the order of k.
 //
 // G lanes to a token (16, 32 or 64, K of them with a route), so a wavefront holds 64 / G tokens.  It
 // writes their rows' zeros, which need no input, in 16-byte pieces while the inputs come, waits for
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(kWaves * 64) void route_backward_kernel(
     }
   }
   const bool on = there && id >= 0 && id < E;
-  if (!on) gw = 0.0f;
+  if (!on) gw = wk = 0.0f;
   float sum = wk * gw;
 #pragma unroll
   for (int o = G / 2; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);

@@ -216,7 +216,7 @@ class MoeMxfp4Layer(_RoutedLayer):
 
 class MoeTrainLayer(_RoutedLayer):
     """The layer over experts in bfloat16 or float16 with its gradients, held on one GPU: forward keeps
-    what backward reads (x itself is held, not copied: it stays as it is until then), and one
+    what backward reads (x and w themselves are held, not copied: they stay as they are until then), and one
     backward follows a forward.  gate_up [E, 2F, H] (gate's F rows, then up's), down [E, H, F] and
     their biases [E, 2F] and [E, H], if any, of one type; contiguous tensors on the device are held, so
     an optimizer's steps on them are seen.  H and F: multiples of 8.  A layer's calls share its

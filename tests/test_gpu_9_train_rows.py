@@ -174,6 +174,27 @@ def test_route_gradient(dtype, T, E, K, gap):
     within(onto, both, err + 2.0 ** -24 * both.abs())
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T,E,K,gap", ROUTES[2:5])
+def test_route_gradient_weight_of_a_route_without_an_expert(T, E, K, gap, value):
+    """Neither the weight nor its gradient of such a route is looked at: the same bits as with zeros."""
+    rng = np.random.default_rng(T + E + 1)
+    idx = np.argsort(rng.standard_normal((T, E)), axis=1)[:, :K].astype(np.int32)
+    idx[rng.random((T, K)) < 0.2] = -1
+    idx[rng.random((T, K)) < 0.1] = E
+    idx[0, 0] = -1
+    idx, gw, w = dev(idx), rand(rng, "float32", T, K), torch.softmax(rand(rng, "float32", T, K), 1)
+    off = (idx < 0) | (idx >= E)
+    got = []
+    for v in (0.0, value):
+        grad = torch.empty(T, E, device="cuda")
+        note(f"route_topk_backward {T}x{E} K={K}, weights without an expert {v}")
+        abi.route_topk_backward(idx, w.masked_fill(off, v), gw.masked_fill(off, v), grad)
+        got.append(grad)
+    assert bool(off.any()) and bool(torch.isfinite(got[0]).all())
+    assert torch.equal(got[0], got[1])
+
+
 def test_route_gradient_against_the_routers_differences():
     """Central differences of the library's own router: the loss is sum w c."""
     T, E, K = 40, 64, 6
