@@ -67,7 +67,7 @@ __device__ __forceinline__ void swiglu_gradient(const v4f& dh, const v4f& g, con
 
 // The row of a that a route reads; the nearest one for a route outside.
 __device__ __forceinline__ int act_row(const MmProblem& p, int route) {
-  return route < 0 ? 0 : min((int)((uint64_t)route * p.k_mul >> p.k_shift), p.n_act - 1);
+  return route_row(route, p.by_k.mul, p.by_k.shift, p.n_act);
 }
 
 // The lane's sum of v over the lanes up to it: within rows of 16 lanes, then over the rows.

@@ -20,7 +20,7 @@ static hipError_t forward(const MmProblem& p, hipStream_t s) {
 
 hipError_t launch_mm_forward(const MmProblem& p_, hipStream_t s) {
   MmProblem p = p_;
-  set_division(p);
+  p.by_k = division_by(p.K);
   return p.dtype == kBF16 ? forward<kBF16>(p, s) : forward<kF16>(p, s);
 }
 

@@ -93,7 +93,7 @@ size_t mm_wgrad_workspace(int rows, int n_out, int k_in, int E) {
 
 hipError_t launch_mm_wgrad(const MmProblem& p_, void* ws, hipStream_t s) {
   MmProblem p = p_;
-  set_division(p);
+  p.by_k = division_by(p.K);
   return p.dtype == kBF16 ? wgrad<kBF16>(p, ws, s) : wgrad<kF16>(p, ws, s);
 }
 

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "mx.hpp"
+#include "route_row.hpp"
 
 namespace moe {
 
@@ -76,14 +77,8 @@ struct MmProblem {
   void* bias_out;          // wgrad: [E x n_out] of out's type, or nullptr
   int n_out, k_in, E, n_act, K, rows;
   int parts;               // wgrad: of each expert's rows, out and bias_out having [E x parts]
-  uint32_t k_mul, k_shift;  // division by K (set_division)
+  Division by_k;           // by K (set by the launcher)
 };
-// n / K = n * k_mul >> k_shift for n < 2^30, K <= 64: k_mul K - 2^k_shift <= K <= 2^(k_shift - 30)
-inline void set_division(MmProblem& p) {
-  p.k_shift = 30;
-  while (1 << (p.k_shift - 30) < p.K) ++p.k_shift;
-  p.k_mul = (uint32_t)(((uint64_t)1 << p.k_shift) / p.K + 1);
-}
 hipError_t launch_mm_forward(const MmProblem& p, hipStream_t s);
 hipError_t launch_mm_dgrad(const MmProblem& p, hipStream_t s);
 hipError_t launch_mm_wgrad(const MmProblem& p, void* ws, hipStream_t s);

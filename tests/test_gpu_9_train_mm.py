@@ -289,3 +289,34 @@ def test_rows_past_31_bits():
     want = [17.0, 0.0, float(rows - 317), float((last * last).sum())]
     assert [dw[e, 5].tolist() for e in range(4)] == [[v] + [0.0] * 7 for v in want]
     assert db[:, n - 1].tolist() == [17.0, 0.0, float(rows - 317), float(last.sum())]
+
+
+# int32's ends among the routes, with rows enough for the few-rows kernel and for the tiles of each size;
+# the last: weight gradients in 256 x 256 tiles with the rows in parts
+STRAYS = [2 ** 31 - 1, 2 ** 30, 2 ** 30 - 1, -1, -2 ** 31, 7, 0, 2 ** 31 - 2, 1]
+
+
+@pytest.mark.parametrize("K", [1, 3, 32, 64])
+@pytest.mark.parametrize("rows,N,k", [(9, 64, 264), (400, 2056, 264), (4500, 2056, 264), (9000, 2056, 264), (3000, 2048, 2048)])
+def test_strays_of_every_size_read_the_nearest_row(rows, N, k, K):
+    n_act = 5
+    rng = np.random.default_rng(rows + K)
+    offsets = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    a = dev(rng.integers(-3, 4, (n_act, k)).astype(np.float32)).bfloat16()
+    w = dev(rng.integers(-3, 4, (1, 2 * N, k)).astype(np.float32)).bfloat16()
+    route = np.resize(np.array(STRAYS, np.int64), rows)
+    route[::5] = rng.integers(0, n_act * K, len(route[::5]))
+    row = dev(np.clip(route, 0, None) // K).clamp(max=n_act - 1)
+    src = dev(route.astype(np.int32))
+    note(f"strays rows={rows} N={N} k={k} K={K}")
+    out, z = torch.empty(rows, N, device="cuda"), torch.empty(rows, 2 * N, device="cuda", dtype=torch.bfloat16)
+    abi.mm_grouped(w[:, :N].contiguous(), offsets, a, out, src=src, K=K)
+    want = a.double()[row] @ w[0].double().t().contiguous()       # whole numbers: sums are exact
+    assert torch.equal(out.double(), want[:, :N])
+    abi.mm_grouped(w, offsets, a, torch.empty(rows, N, device="cuda", dtype=torch.bfloat16), src=src, K=K, swiglu=True, z=z)
+    assert torch.equal(z, want.bfloat16())
+    g = dev(rng.integers(-3, 4, (rows, N)).astype(np.float32)).bfloat16()
+    size = abi.mm_grouped_wgrad_workspace_size(rows, N, k, 1)
+    ws, dw = torch.empty(size, dtype=torch.uint8, device="cuda"), torch.empty(1, N, k, device="cuda")
+    abi.mm_grouped_wgrad(g, offsets, a, dw, ws, src=src, K=K)
+    assert torch.equal(dw[0].double(), g.double().t().contiguous() @ a.double()[row])
