@@ -13,6 +13,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "route_row.hpp"
+
 namespace moe {
 
 constexpr int kMxBlock = 32;   // values per scale
@@ -74,7 +76,7 @@ struct MxProblem {
   uint8_t* out_scales;     // SwiGLU: the requantised rows' scale bytes
   int n_out;               // output columns
   int k_in, E, n_act, K, rows;
-  uint32_t k_mul, k_shift;  // division by K (set by the launcher)
+  Division by_k;           // by K (set by the launcher)
   int epilogue;            // kMxF32, kMxBF16, kMxSwiglu (n_mat = 2 n_out: gate, then up)
 };
 constexpr int kMxF32 = 0, kMxBF16 = 1, kMxSwiglu = 2;

@@ -97,8 +97,7 @@ __global__ __launch_bounds__(256) void mx_mm_narrow_kernel(MxProblem p, bool by_
   const int n0 = blockIdx.y * 32;
   const size_t kb = p.k_in / 2, sb = p.k_in / kMxBlock;
   int r = t.row0 + min(l32, t.nrows - 1);
-  if (p.src) r = p.src[r] < 0 ? 0 : (int)((uint64_t)p.src[r] * p.k_mul >> p.k_shift);
-  r = min(r, p.n_act - 1);
+  r = p.src ? route_row(p.src[r], p.by_k.mul, p.by_k.shift, p.n_act) : min(r, p.n_act - 1);
   const uint8_t* a = p.a + (size_t)r * kb + 32 * half;
   const uint8_t* as = p.as + (size_t)r * sb + 2 * half;
   const size_t wrow = (size_t)t.expert * p.n_out * kMats + n0 + l32;
@@ -657,8 +656,8 @@ __global__ __launch_bounds__(G::kWaves * 64, G::kMinWaves) void mx_mm_wide_kerne
       at = 2;
     } else if (at == 2) {
       auto act = [&](uint32_t r) -> uint32_t {
-        const uint32_t row = p.src ? (uint32_t)((uint64_t)r * p.k_mul >> p.k_shift) : r;
-        return (int)r < 0 ? 0u : min(row, (uint32_t)(p.n_act - 1));
+        return p.src ? route_row((int32_t)r, p.by_k.mul, p.by_k.shift, p.n_act)
+                     : min(r, (uint32_t)(p.n_act - 1));
       };
       plan_rows<G, WIDE, false>(e, p.k_in, act, wave, here(lane));
       auto wrow = [&](int i) -> uint32_t {  // the expert's matrix row in row i of the tile
@@ -802,11 +801,7 @@ hipError_t launch_wide_any(const MxProblem& p, hipStream_t s) {
 // tiles would not fill the CUs twice; then the tile's height goes by the rows an expert has.
 hipError_t launch_mx_mm(const MxProblem& p_, hipStream_t s) {
   MxProblem p = p_;
-  // n / K = n * k_mul >> k_shift for n < 2^30, K <= 64: k_mul K - 2^k_shift <= K <= 2^(k_shift -
-  // 30)
-  p.k_shift = 30;
-  while (1 << (p.k_shift - 30) < p.K) ++p.k_shift;
-  p.k_mul = (uint32_t)(((uint64_t)1 << p.k_shift) / p.K + 1);
+  p.by_k = division_by(p.K);
   auto tiles = [&](int high) { return std::min<int64_t>(p.rows, (int64_t)p.rows / high + p.E); };
   if (tiles(32) * (p.n_out / 32) <= 3 * kCus) return launch_narrow(p, s);
   const int64_t feat = p.epilogue == kMxSwiglu ? 128 : 256;

@@ -3,7 +3,6 @@
 #pragma once
 
 #include "mx.hpp"
-#include "route_row.hpp"
 
 namespace moe {
 
