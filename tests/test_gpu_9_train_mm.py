@@ -320,3 +320,30 @@ def test_strays_of_every_size_read_the_nearest_row(rows, N, k, K):
     ws, dw = torch.empty(size, dtype=torch.uint8, device="cuda"), torch.empty(1, N, k, device="cuda")
     abi.mm_grouped_wgrad(g, offsets, a, dw, ws, src=src, K=K)
     assert torch.equal(dw[0].double(), g.double().t().contiguous() @ a.double()[row])
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+def test_gradients_of_large_gates_and_ups(rows):
+    """Finite gates, ups and gradients whose product without the sigmoid leaves fp32's range: the gradient is
+    finite wherever the definition's is, and 0 far on the negative side."""
+    gates = [-3e38, -1e36, -1e20, -200.0, -89.0, -86.0, -80.0, -40.0, -3.0, 0.0, 3.0, 90.0, 1e4, -1e37, 5.0, -87.0]
+    ups = [1.0, -1e36, 3e38, 1e-3]
+    n = len(gates) * len(ups)
+    z = torch.empty(rows, 2 * n, device="cuda", dtype=torch.bfloat16)
+    z[:, :n] = torch.tensor(gates, device="cuda").repeat_interleave(len(ups)).bfloat16()
+    z[:, n:] = torch.tensor(ups, device="cuda").repeat(len(gates)).bfloat16()
+    w = torch.eye(n, device="cuda").bfloat16().unsqueeze(0)
+    offsets = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    for d in (1e4, 1e38, -1e-4):
+        grad = torch.full((rows, n), d, device="cuda").bfloat16()
+        out = torch.empty_like(z)
+        note(f"large gates rows={rows} d={d}")
+        abi.mm_grouped_dgrad(w, offsets, grad, out, z=z)
+        g, u = z[:, :n].double(), z[:, n:].double()
+        dg, eg, du, eu = swiglu_grad(grad.double(), g, u, torch.zeros_like(g))
+        top = float(torch.finfo(torch.bfloat16).max)
+        for got, want, err in ((out[:, :n], dg, eg), (out[:, n:], du, eu)):
+            fits = want.abs() + err < top / 2
+            within(got[fits], want[fits], err[fits])
+            assert bool((got[g < -100] == 0).all()) and not bool(got.isnan().any())
+        assert 2 * int(fits.sum()) > fits.numel()
