@@ -262,12 +262,16 @@ class MoeTrainLayer(_RoutedLayer):
     def forward(self, x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor,
                 out: torch.Tensor | None = None, residual: torch.Tensor | None = None):
         """out [T, H] (float32 or the experts' type, which is the default) = residual (of out's type)
-        + the layer of x [T, H] of the experts' type."""
+        + the layer of x [T, H] of the experts' type.  out may not lie over x or w."""
         T = self._tokens(x, idx)
-        if out is None:
+        given = out is not None
+        if not given:
             out = torch.empty((T, self.H), dtype=self.dtype, device=self.device)
         self._want(("w", w, torch.float32, (T, self.K)))
         self._rows(("x", x, self.dtype), ("out", out, out.dtype), ("residual", residual, out.dtype))
+        for name, t in (("x", x), ("w", w)):
+            if given and _share(out, t):
+                raise ValueError(f"out: memory apart from {name}'s is wanted, which backward reads")
         R = T * self.K
         src, slot = self.src[:R], self.slot[:R]
         z, h, rows = self.z[:R], self.h[:R], self.rows[:R]
@@ -346,6 +350,23 @@ def _mx_bytes(name: str, a, own, device) -> torch.Tensor:
     if t.dtype not in (torch.uint8, own):
         raise ValueError(f"{name}: uint8 or {own} is wanted, not {t.dtype}")
     return t.view(torch.uint8).to(device).contiguous()
+
+
+def _share(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two matrices of contiguous rows have a byte in common."""
+    def rows_of(t):
+        row, n = t.shape[1] * t.element_size(), t.shape[0]
+        return t.data_ptr(), row, n, t.stride(0) * t.element_size() if n > 1 else row
+
+    (pa, ra, na, la), (pb, rb, nb, lb) = rows_of(a), rows_of(b)
+    if pa + (na - 1) * la + ra <= pb or pb + (nb - 1) * lb + rb <= pa:
+        return False
+    # columns of one buffer, say: of each row of b, a's last row that starts no later and the next one
+    at = pb - pa + lb * np.arange(nb, dtype=np.int64)
+    i = np.clip(at // la, -1, na - 1)
+    before = (i >= 0) & (at < i * la + ra)
+    after = (i + 1 < na) & (at + rb > (i + 1) * la)
+    return bool((before | after).any())
 
 
 def _to_device(a, dtype, device):

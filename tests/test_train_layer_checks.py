@@ -1,0 +1,86 @@
+"""What MoeTrainLayer refuses before anything is enqueued (CPU only: the library's calls are recorded, not
+made)."""
+import numpy as np
+import pytest
+import torch
+
+from quantized_expert_grouped_amd import abi, layer
+from quantized_expert_grouped_amd.layer import MoeTrainLayer
+
+E, F, H, K, T = 3, 128, 256, 2, 6
+B16 = torch.bfloat16
+CALLS = ("build_maps", "mm_grouped", "mm_grouped_dgrad", "mm_grouped_wgrad", "combine_rows", "combine_rows_backward",
+         "route_topk_backward")
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    done = []
+    monkeypatch.setattr(abi, "_on_current", lambda t: t.get_device())
+    abi._dtypes()
+    for name in CALLS:
+        monkeypatch.setattr(abi, name, lambda *a, name=name, **k: done.append(name))
+    return done
+
+
+def make(**kw):
+    args = dict(gate_up=torch.zeros(E, 2 * F, H, dtype=B16), down=torch.zeros(E, H, F, dtype=B16), max_tokens=8, K=K,
+                device="cpu")
+    return MoeTrainLayer(**{**args, **kw})
+
+
+def routes():
+    return torch.zeros(T, K, dtype=torch.int32), torch.zeros(T, K)
+
+
+def test_sharing_of_memory_is_exact():
+    """Against the bytes themselves, for matrices anywhere in one small buffer."""
+    rng = np.random.default_rng(0)
+    buf, seen = torch.zeros(200, dtype=torch.uint8), [0, 0]
+    for _ in range(4000):
+        m = []
+        for _ in range(2):
+            size = int(rng.choice([1, 2, 4]))
+            cols, n = int(rng.integers(1, 6)), int(rng.integers(1, 6))
+            ld = cols + int(rng.integers(0, 9))
+            room = 200 // size - ((n - 1) * ld + cols)
+            if room < 0:
+                break
+            t = buf.view({1: torch.uint8, 2: B16, 4: torch.float32}[size])
+            m.append(t[int(rng.integers(0, room + 1)):].as_strided((n, cols), (ld, 1)))
+        if len(m) < 2:
+            continue
+        bytes_of = [{t.data_ptr() + (r * t.stride(0) + c) * t.element_size() + b for r in range(t.shape[0])
+                     for c in range(t.shape[1]) for b in range(t.element_size())} for t in m]
+        want = bool(bytes_of[0] & bytes_of[1])
+        assert layer._share(*m) == layer._share(*m[::-1]) == want
+        seen[want] += 1
+    assert min(seen) > 300
+
+
+def test_out_over_what_backward_reads_is_refused(calls):
+    la, (idx, w) = make(), routes()
+    both = torch.zeros(2 * T, H, dtype=B16)
+    x = both[2:2 + T]
+    for kw in (dict(out=x), dict(out=x, residual=x), dict(out=both[:T]), dict(out=both[T:], residual=both[T:]),
+               dict(out=both.view(-1)[2 * H + 8:][:T * H].view(T, H))):
+        with pytest.raises(ValueError, match="apart from x"):
+            la.forward(x, idx, w, **kw)
+    buf = torch.zeros(T * H)
+    w = buf[H:H + T * K].view(T, K)
+    with pytest.raises(ValueError, match="apart from w"):
+        la.forward(x, idx, w, out=buf.view(T, H))
+    assert not calls and la.kept is None
+
+
+def test_out_beside_x_is_taken(calls):
+    """Columns of one buffer, the buffer's other rows, the residual itself; one token next to another."""
+    la, (idx, w) = make(), routes()
+    wide, tall = torch.zeros(T, 2 * H, dtype=B16), torch.zeros(2 * T, H, dtype=B16)
+    other = torch.zeros(T, H)
+    for x, out, residual in ((wide[:, :H], wide[:, H:], None), (tall[:T], tall[T:], tall[T:]), (tall[T:], other, other),
+                             (tall[::2], tall[1::2], None)):
+        del calls[:]
+        assert la.forward(x, idx, w, out=out, residual=residual) is out
+        assert calls == ["build_maps", "mm_grouped", "mm_grouped", "combine_rows"]
+    la.forward(tall[:1], idx[:1], w[:1], out=tall[1:2])
