@@ -262,7 +262,8 @@ class MoeTrainLayer(_RoutedLayer):
     def forward(self, x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor,
                 out: torch.Tensor | None = None, residual: torch.Tensor | None = None):
         """out [T, H] (float32 or the experts' type, which is the default) = residual (of out's type)
-        + the layer of x [T, H] of the experts' type.  out may not lie over x or w."""
+        + the layer of x [T, H] of the experts' type.  out may not lie over x or w;
+        it may be residual itself."""
         T = self._tokens(x, idx)
         given = out is not None
         if not given:
@@ -272,6 +273,9 @@ class MoeTrainLayer(_RoutedLayer):
         for name, t in (("x", x), ("w", w)):
             if given and _share(out, t):
                 raise ValueError(f"out: memory apart from {name}'s is wanted, which backward reads")
+        if given and residual is not None and _share(out, residual) and (
+                out.data_ptr() != residual.data_ptr() or T > 1 and out.stride(0) != residual.stride(0)):
+            raise ValueError("out: residual's very rows or memory apart from them are wanted")
         R = T * self.K
         src, slot = self.src[:R], self.slot[:R]
         z, h, rows = self.z[:R], self.h[:R], self.rows[:R]

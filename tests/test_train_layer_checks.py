@@ -84,3 +84,19 @@ def test_out_beside_x_is_taken(calls):
         assert la.forward(x, idx, w, out=out, residual=residual) is out
         assert calls == ["build_maps", "mm_grouped", "mm_grouped", "combine_rows"]
     la.forward(tall[:1], idx[:1], w[:1], out=tall[1:2])
+
+
+def test_out_partly_over_residual_is_refused(calls):
+    """The same address with other strides, rows or columns further on."""
+    la, (idx, w) = make(), routes()
+    x, buf = torch.zeros(T, H, dtype=B16), torch.zeros(4 * T * H)
+    out = buf.as_strided((T, H), (H, 1))
+    for residual in (buf.as_strided((T, H), (2 * H, 1)), buf.as_strided((T, H), (H, 1), H),
+                     buf.as_strided((T, H), (H, 1), 8), buf.as_strided((T, H), (2 * H, 1), (T - 1) * H)):
+        for kw in (dict(out=out, residual=residual), dict(out=residual, residual=out)):
+            with pytest.raises(ValueError, match="residual's very rows"):
+                la.forward(x, idx, w, **kw)
+    assert not calls and la.kept is None
+    la.forward(x, idx, w, out=buf.as_strided((T, H), (2 * H, 1)), residual=buf.as_strided((T, H), (2 * H, 1), H))
+    la.forward(x[:1], idx[:1], w[:1], out=buf.as_strided((1, H), (H, 1)), residual=buf.as_strided((1, H), (8, 1)))
+    assert calls == 2 * ["build_maps", "mm_grouped", "mm_grouped", "combine_rows"]
