@@ -240,8 +240,10 @@ class MoeTrainLayer(_RoutedLayer):
             raise ValueError(f"H and F are multiples of 8, K one of 1 .. E, {abi.MAX_K} at most")
         if self.E > abi.MAX_E:
             raise ValueError(f"E={self.E} exceeds {abi.MAX_E}")
-        if max_tokens < 1:
-            raise ValueError("max_tokens is at least 1")
+        if not 1 <= max_tokens <= 1 << 23:
+            raise ValueError("max_tokens is one of 1 .. 2^23")
+        if max(f2, self.H) >= 1 << 21 or f2 * self.H * 2 >= 1 << 31:
+            raise ValueError("an expert's matrix of less than 2 GiB is wanted, 2F and H below 2^21")
         self._buffers(max_tokens, K)
         R = max_tokens * K
         self.z, self.h, self.rows = (torch.empty((R, n), dtype=self.dtype, device=self.device)
@@ -257,7 +259,10 @@ class MoeTrainLayer(_RoutedLayer):
         if t.dtype != self.dtype or t.shape != shape:
             raise ValueError(f"{name}: {self.dtype} {tuple(shape)} is wanted, not {t.dtype} "
                              f"{tuple(t.shape)}")
-        return t.detach().to(self.device).contiguous()
+        t = t.detach().to(self.device).contiguous()
+        if t.data_ptr() % 16:
+            raise ValueError(f"{name}: an address that is a multiple of 16 is wanted")
+        return t
 
     def forward(self, x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor,
                 out: torch.Tensor | None = None, residual: torch.Tensor | None = None):
@@ -270,6 +275,10 @@ class MoeTrainLayer(_RoutedLayer):
             out = torch.empty((T, self.H), dtype=self.dtype, device=self.device)
         self._want(("w", w, torch.float32, (T, self.K)))
         self._rows(("x", x, self.dtype), ("out", out, out.dtype), ("residual", residual, out.dtype))
+        ld = x.stride(0) if T > 1 else self.H
+        if ld >= 1 << 21 or ((T - 1) * ld + self.H) * 2 >= 1 << 31:
+            raise ValueError("x: less than 2 GiB from the first row to the last is wanted, and rows less "
+                             "than 2^21 values apart")
         for name, t in (("x", x), ("w", w)):
             if given and _share(out, t):
                 raise ValueError(f"out: memory apart from {name}'s is wanted, which backward reads")

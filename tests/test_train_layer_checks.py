@@ -100,3 +100,45 @@ def test_out_partly_over_residual_is_refused(calls):
     la.forward(x, idx, w, out=buf.as_strided((T, H), (2 * H, 1)), residual=buf.as_strided((T, H), (2 * H, 1), H))
     la.forward(x[:1], idx[:1], w[:1], out=buf.as_strided((1, H), (H, 1)), residual=buf.as_strided((1, H), (8, 1)))
     assert calls == 2 * ["build_maps", "mm_grouped", "mm_grouped", "combine_rows"]
+
+
+def test_what_the_products_do_not_take_is_refused_before_the_maps(calls):
+    """Of the layer's weights and sizes when it is made, of x by the forward (no value is touched: the large
+    tensors are address space alone)."""
+    odd = torch.zeros(E * 2 * F * H + 8, dtype=B16)
+    for at in (1, 4, 7):
+        with pytest.raises(ValueError, match="gate_up: an address"):
+            make(gate_up=odd[at:at + E * 2 * F * H].view(E, 2 * F, H))
+    with pytest.raises(ValueError, match="gate_up_bias: an address"):
+        make(gate_up_bias=torch.zeros(E * 2 * F + 1, dtype=B16)[1:].view(E, 2 * F))
+    assert make(gate_up=odd[8:].view(E, 2 * F, H)).E == E
+    for h, f in ((1 << 15, 1 << 14), (1 << 21, 8), (8, 1 << 20)):
+        with pytest.raises(ValueError, match="less than 2 GiB"):
+            make(gate_up=torch.empty(1, 2 * f, h, dtype=B16), down=torch.empty(1, h, f, dtype=B16), K=1, max_tokens=1)
+    with pytest.raises(ValueError, match="max_tokens"):
+        make(max_tokens=(1 << 23) + 1)
+    la = make(gate_up=torch.zeros(1, 16, 8, dtype=B16), down=torch.zeros(1, 8, 8, dtype=B16), K=1, max_tokens=1 << 12)
+    for t, ld in ((2, 1 << 21), (1 << 12, (1 << 18) + 264), ((1 << 11) + 1, 1 << 19)):
+        x = torch.empty((t - 1) * ld + 8, dtype=B16).as_strided((t, 8), (ld, 1))
+        with pytest.raises(ValueError, match="x: less than 2 GiB"):
+            la.forward(x, torch.zeros(t, 1, dtype=torch.int32), torch.zeros(t, 1))
+    assert not calls and la.kept is None
+    t, ld = 1 << 11, 1 << 19                                     # the largest below
+    x = torch.empty((t - 1) * ld + 8, dtype=B16).as_strided((t, 8), (ld, 1))
+    la.forward(x, torch.zeros(t, 1, dtype=torch.int32), torch.zeros(t, 1))
+    la.forward(x[:1].as_strided((1, 8), (1 << 22, 1)), torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, 1))
+    assert len(calls) == 8
+
+
+def test_the_librarys_own_limits_are_the_layers():
+    """The sizes on both sides of the layer's limits, put to the C entry points (made-up pointers, refused or
+    not before anything is followed: a size that is taken is not called)."""
+    P, lib = 1 << 20, abi.lib()
+
+    def mm(n_act, lda, k=8, n=8, w=P):
+        return lib.moe_mm_grouped(w, 1, n, k, P, 1, P, lda, n_act, P, 1, 1, None, 1, None, 0, None, 0, P, 1, n, None)
+
+    assert mm(2, 1 << 21) == mm(1 << 12, (1 << 18) + 264) == mm((1 << 11) + 1, 1 << 19) == -2
+    assert mm(4, 8, k=1 << 15, n=1 << 14) == mm(4, 1 << 21, k=1 << 21) == -2 and mm(4, 8, w=P + 8) == -1
+    assert lib.moe_mm_grouped_wgrad_workspace_size(1 << 20, 1 << 21, 8, 1) == 0
+    assert lib.moe_combine_rows(P, 1, 8, 8, P, P, (1 << 23) + 1, 1, 8, None, 0, P, 1, 8, None) == -2
