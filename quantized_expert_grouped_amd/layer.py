@@ -347,9 +347,12 @@ class MoeTrainLayer(_RoutedLayer):
 
     def route_backward(self, idx: torch.Tensor, w: torch.Tensor, grad_w: torch.Tensor,
                        grad_logits: torch.Tensor | None = None) -> torch.Tensor:
-        """The gradient of route's logits from its weights'; onto grad_logits (balance's, say), if
+        """The gradient [T, E] of route's logits from its weights'; onto grad_logits (balance's, say), if
         given."""
         onto = grad_logits is not None
+        if onto and grad_logits.shape != (idx.shape[0], self.E):
+            raise ValueError(f"grad_logits: {(idx.shape[0], self.E)} is wanted, not "
+                             f"{tuple(grad_logits.shape)}")
         if not onto:
             grad_logits = self._f32(idx.shape[0], self.E)
         abi.route_topk_backward(idx, w, grad_w, grad_logits, accumulate=onto)

@@ -142,3 +142,14 @@ def test_the_librarys_own_limits_are_the_layers():
     assert mm(4, 8, k=1 << 15, n=1 << 14) == mm(4, 1 << 21, k=1 << 21) == -2 and mm(4, 8, w=P + 8) == -1
     assert lib.moe_mm_grouped_wgrad_workspace_size(1 << 20, 1 << 21, 8, 1) == 0
     assert lib.moe_combine_rows(P, 1, 8, 8, P, P, (1 << 23) + 1, 1, 8, None, 0, P, 1, 8, None) == -2
+
+
+def test_router_gradient_of_another_expert_count_is_refused(calls):
+    """Routes to the layer's last experts would be lost in fewer columns without a word."""
+    la, (idx, w) = make(), routes()
+    for shape in ((T, E - 1), (T, E + 1), (T - 1, E), (T * E,)):
+        with pytest.raises(ValueError, match="grad_logits"):
+            la.route_backward(idx, w, w, torch.zeros(shape))
+    assert not calls
+    assert la.route_backward(idx, w, w).shape == la.route_backward(idx, w, w, torch.zeros(T, E)).shape == (T, E)
+    assert calls == 2 * ["route_topk_backward"]
