@@ -199,3 +199,15 @@ def test_parameters_that_require_gradients_are_taken():
     w = torch.nn.Parameter(torch.zeros(3, 256, 256, dtype=torch.bfloat16))
     la = make(gate_up=w)
     assert not la.gate_up.requires_grad and la.gate_up.data_ptr() == w.data_ptr()
+
+
+@pytest.mark.parametrize("N,k,E", [(64, 64, 1), (1024, 1024, 1), (2048, 2048, 1), (512, 512, 4)])
+def test_weight_gradient_with_parts_refuses_what_is_no_workspace(calls, N, k, E):
+    """Sizes whose rows are taken in parts, which the workspace holds (256 x 256 tiles among them)."""
+    kw = dict(n_out=N, ldg=N, k_in=k, lda=k, E=E, rows=8192, n_act=8192)
+    need = abi.mm_grouped_wgrad_workspace_size(8192, N, k, E)
+    assert need > E * N * k * 4                                 # two parts at least
+    refused(calls["wgrad"], EWORKSPACE, [dict(kw, ws_bytes=v) for v in (need - 1, need // 2, 0)])
+    refused(calls["wgrad"], EINVAL, [dict(kw, ws=None, ws_bytes=need), dict(kw, ws=P + 8, ws_bytes=need),
+                                     dict(kw, ws=None, ws_bytes=0)])
+    assert abi.mm_grouped_wgrad_workspace_size(255 * E, N, k, E) == 0   # one part
