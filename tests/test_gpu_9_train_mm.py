@@ -347,3 +347,43 @@ def test_gradients_of_large_gates_and_ups(rows):
             within(got[fits], want[fits], err[fits])
             assert bool((got[g < -100] == 0).all()) and not bool(got.isnan().any())
         assert 2 * int(fits.sum()) > fits.numel()
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("rows", [400, 17000, 33000])
+def test_gates_from_one_end_to_the_other_in_the_tiles(rows, dtype):
+    """As for one row, through the tiles' own epilogues: 128 x 128, forward in 256 x 256, both in 256 x 256."""
+    n = 512
+    g = torch.linspace(-120, 120, n, device="cuda").to(DT[dtype])
+    one = torch.ones(rows, 8, device="cuda", dtype=DT[dtype])
+    offsets = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    w = torch.zeros(1, 2 * n, 8, device="cuda", dtype=DT[dtype])
+    w[0, :n, 0], w[0, n:, 1] = g, 1.0
+    out, z = (torch.empty(rows, c, device="cuda", dtype=DT[dtype]) for c in (n, 2 * n))
+    note(f"gates in tiles rows={rows} {dtype}")
+    abi.mm_grouped(w, offsets, one, out, swiglu=True, z=z)
+    assert bool((z[:, :n] == g).all()) and bool((z[:, n:] == 1).all())
+    y = g.double().unsqueeze(0)
+    zero = torch.zeros_like(y)
+    within(out[:1], *swiglu(y, torch.ones_like(y), zero, zero))
+    assert torch.equal(out, out[:1].expand_as(out))
+    eye = torch.eye(n, device="cuda").to(DT[dtype]).unsqueeze(0)
+    back = torch.empty_like(z)
+    abi.mm_grouped_dgrad(eye, offsets, torch.ones(rows, n, device="cuda", dtype=DT[dtype]), back, z=z)
+    dg, eg, du, eu = swiglu_grad(torch.ones_like(y), y, torch.ones_like(y), zero)
+    within(back[:1, :n], dg, eg)
+    within(back[:1, n:], du, eu)
+    assert torch.equal(back, back[:1].expand_as(back))
+
+
+# as SHAPES: 64 to 128 tiles of 256 x 256, so their rows come in parts
+PARTS = [(1500, 2, 2, 2048, 1032, True, 0.0, 0.1, 8), (3000, 1, 1, 2056, 2048, True, 0.0, 0.0, 0),
+         (4000, 2, 2, 1536, 1544, True, 2.0, 0.0, 0), (2100, 3, 3, 1032, 1800, False, 0.0, 0.2, 16),
+         (3000, 1, 2, 1544, 1536, False, 4.0, 0.0, 0)]
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("T,K,E,N,k,gather,skew,pad,gap", PARTS)
+def test_weight_gradient_in_parts_of_large_tiles(dtype, T, K, E, N, k, gather, skew, pad, gap):
+    assert abi.mm_grouped_wgrad_workspace_size(T * K, N, k, E) > 0
+    test_weight_gradient(dtype, T, K, E, N, k, gather, skew, pad, gap)
