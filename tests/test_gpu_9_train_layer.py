@@ -283,3 +283,19 @@ def test_refusals_leave_nothing_enqueued(monkeypatch):
     with pytest.raises(ValueError):
         c.layer.forward(x, idx, w[:, :1])
     assert not done and c.layer.kept is None
+
+
+def test_every_iteration_on_two_streams():
+    """As test_two_layers_on_two_streams, with each iteration's results compared."""
+    cases = [Case(*SIZES[2], seed=3), Case(*SIZES[3], seed=4)]
+    want = [bits(c.step()) for c in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for c, st in zip(cases, streams):
+            with torch.cuda.stream(st):
+                got.append(c.step())
+    torch.cuda.synchronize()
+    for i, r in enumerate(got):
+        assert same(bits(r), want[i % 2]), i
