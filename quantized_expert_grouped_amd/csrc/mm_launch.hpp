@@ -52,8 +52,12 @@ hipError_t launch_small(const MmProblem& p, hipStream_t s) {
     if (most_tiles<Small<OP>>(p) <= kCus) return launch_geo<OP, DT, ODT, SWIGLU, Deep<OP>>(p, s);
   return launch_geo<OP, DT, ODT, SWIGLU, Small<OP>>(p, s);
 }
-// Large where it fills the CUs and an expert has more than 64 rows in the mean (2048 -> 2 x 512, 512
-// experts, 40 rows each: 400 us in 128 x 128, 433 in 256 x 256; 160 rows: 722, 585).
+// Large where it fills the CUs and an expert has more than 64 rows in the mean.  In us, 128 x 128 and 256 x
+// 256, by rows of each expert (where the border lies goes by the sizes, and none is right for all):
+//   512 experts, 2048 -> 2 x 512   forward   40: 374, 413   64: 401, 433   96: 432, 463   160: 607, 520
+//                                  dgrad     40: 445, 462   64: 502, 486   96: 519, 503   160: 651, 559
+//   64 experts, 2048 -> 2048       forward   40: 132, 139   64: 134, 140   96: 140, 148   160: 184, 159
+//                                  dgrad     40: 105, 113   64: 111, 114   96: 121, 122   160: 160, 133
 template <int OP, int DT, int ODT, bool SWIGLU>
 hipError_t launch_tiles(const MmProblem& p, hipStream_t s) {
   const bool few_rows = p.rows / p.E <= 64;

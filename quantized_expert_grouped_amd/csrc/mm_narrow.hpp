@@ -160,11 +160,14 @@ inline int columns(const MmProblem& p) { return (p.n_out + kCols - 1) / kCols; }
 // Whether it beats the 128 x 128 tiles, by sizes alone.  It reads a matrix once for each 16 rows, at
 // about 4.5 TB/s and 5 us more; a tile of few rows takes 12 us for each 1024 of k, however few there
 // are, and reads a matrix once (us, narrow and tiles; rows spread over E experts):
-//   4096 -> 4096, E = 1         1 row 10, 50;  16 rows 20, 51;  64 rows 46, 53;  128 rows 81, 39
-//   2048 -> 2048, E = 8         2 rows 7, 27;  64 rows 27, 29;  128 rows 40, 30
-//   1024 -> 1024, E = 64        8 rows 7, 16;  16 rows 12, 17;  32 rows 19, 18;  64 rows 34, 18
-//   512 -> 2048, E = 512        10 rows 9, 12;  20 rows 17, 13;  80 rows 55, 38
-//   2048 -> 2 x 512, E = 512    10 rows 16, 19;  80 rows 69, 85;  160 rows 122, 128;  320 rows 227, 187
+//   4096 -> 4096, E = 1        rows 1: 10, 50   16: 20, 50   64: 46, 53   80: 55, 53   96: 63, 54   128: 80, 40
+//   2048 -> 2048, E = 8        2: 7, 27   8: 17, 28   64: 23, 29   96: 25, 29   128: 40, 29
+//   1024 -> 1024, E = 64       8: 7, 16   16: 12, 17   24: 14, 18   32: 19, 19   64: 35, 23
+//   512 -> 2048, E = 512       10: 8, 10   16: 16, 11   20: 16, 13   80: 54, 31
+//   2048 -> 2 x 512, E = 512   10: 14, 18   80: 63, 71   120: 105, 88   160: 121, 119   200: 149, 160   320: 236, 214
+// It is taken up to 95, 79, 23, 12 and 170 rows of these.  On the wrong side lie 80 to 95 rows of the first
+// (2 us), 80 to 100 of the second (5), 24 of the third (4) and, the times being uneven, 120 (17) and 200 (11)
+// of the last.
 inline bool wins(const MmProblem& p) {
   if (columns(p) > 65535) return false;
   const int64_t tiles = std::min(p.rows, p.E) + p.rows / kRows;

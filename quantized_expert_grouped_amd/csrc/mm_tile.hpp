@@ -10,10 +10,12 @@
 // A piece that is not there (past the matrix's edge, the last row, the end of c) has an offset past
 // the buffer descriptor's size, for which the load writes zeros without a fetch.
 //
-// What bounds it (us, MI355X): 8191 x 4096 x 4096 forward 237 to 243 (1130 to 1160 TFLOP/s; the matrix
-// cores are busy for 61% of the cycles, LDS reads find no bank conflict), dgrad 226 to 243, wgrad 242
-// to 250; 8192 tokens, K = 10, 512 experts, 2048 -> 2 x 512: memory, 2.4 GB in 547 to 590, dgrad 577,
-// wgrad 780 with 2.1 GB to write.
+// What bounds it (us, MI355X): 8191 x 4096 x 4096 forward 226 to 243 (1130 to 1215 TFLOP/s; the matrix
+// cores are busy for 61% of the cycles, LDS reads find no bank conflict), dgrad 224 to 243, wgrad 223
+// to 250.  8192 tokens, K = 10, 512 experts, 2048 -> 2 x 512: memory in the forward, 2.4 GB in 547 to
+// 590, and in dgrad, 2.65 GB in 577 to 591; wgrad, 2.35 GB (2.1 written) in 771 to 780, is bound by
+// neither memory nor the matrix cores (3.0 TB/s; busy for 20% of the cycles): a tile is five or six stages
+// and then 128 KB of results, and the one workgroup of a CU has nothing else to do while they drain.
 //
 // Workgroups stay and walk through the tiles.  Loads run as many stages ahead of the products as
 // there are buffers, over the tiles' ends: a stage's go out into the buffer whose reads have just

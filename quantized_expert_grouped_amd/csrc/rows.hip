@@ -228,7 +228,10 @@ Shape shape_of(int rows, int H, int rows_a_thread) {
 
 template <class V>
 void dispatch(const DispatchArgs& a, hipStream_t s) {
-  // few rows: one a thread, for more workgroups (a batch of 17 tokens, K = 10)
+  // Few rows: one a thread, for more workgroups (kernels in a row, one and four rows a thread, us: 170
+  // rows of 2048 bf16 2.0, 2.7; 2000 rows 3.5, 3.7; 4000 rows 4.6, 4.6; 8000 rows 7.1, 6.7; of 8192
+  // values 600 rows 3.7, 4.0, 2000 rows 7.3, 7.0, 8000 rows 30.8, 31.4; 80,000 rows of 256 14.9, 11.6,
+  // of 2048 86.5, 89.5).
   if (a.rows < 4096) {
     const Shape g = shape_of(a.rows, a.H, 1);
     dispatch_kernel<V, 1><<<g.grid, g.block, 0, s>>>(a);
